@@ -22,6 +22,12 @@
  *                                     verify step of speculative decoding)
  *   kv_cache_store_fp8, paged_decode_attention_fp8(_store)  the same over E4M3
  *                                     (FP8) pools
+ *   kv_cache_store_norm_rope(_fp8)    the norm of query and key heads, the rotation
+ *                                     by position and the store, in one pass
+ *   paged_decode_attention_scored(_fp8), paged_prefill_attention_scored
+ *                                     attention whose scores are capped, biased by
+ *                                     distance, or restricted by a window, documents
+ *                                     or a two-way prefix (pkv_score_options)
  *   kv_cache_copy_blocks              copy-on-write block copies
  *   paged_decode_attention_noalloc    decode without a caller workspace
  *   pkv_testing_set_wait_fault        tests only: make a bounded wait run out
@@ -405,6 +411,137 @@ int paged_prefill_attention(void* out, float* lse, const void* q,
                             int B, int max_seqlen_q, int max_seqlen_k, int Hq,
                             int Hkv, int D, int block_size, int64_t num_blocks,
                             float scale, pkv_stream_t stream);
+
+/* kv_cache_store_norm_rope — what a layer does to a projection's q, k and v
+ * before it attends: the RMS norm of every query and key head, the rotation by
+ * position, and kv_cache_store of the keys and values, in one pass over the
+ * data.  The source pages store K/V that are already rotated ("Nano-vLLM System
+ * Architecture Analysis", §2 Core Components, "Attention with Paged Cache") and
+ * do not describe the step.
+ *
+ * For token t and a query or key head row x (128 values), in fp32:
+ *   y = x * rsqrt(mean(x^2) + eps) * w, w = q_weight or k_weight; a NULL weight
+ *       leaves that tensor's heads as they are (y = x);
+ *   the first rotary_dim dims of y are rotated pair by pair: with R = rotary_dim
+ *       and i in [0, R/2), the pair (a, b) is (y[i], y[i + R/2]), or
+ *       (y[2i], y[2i+1]) when interleaved != 0, and becomes
+ *       (a c - b s, b c + a s) with c = cos_sin[positions[t]][i] and
+ *       s = cos_sin[positions[t]][R/2 + i]; dims past R keep y.
+ * q_out[t, h, :] is the result rounded to bf16, for every t with a valid
+ * position (a slot below 0 does not matter).  Keys rounded to bf16 and values
+ * bit for bit go to slot_mapping[t] under kv_cache_store's slot rules.
+ * q            : bf16 rows [T, Hq, 128] at q + t*q_tok_stride; k, v likewise with
+ *                Hkv heads (the three may be slices of one packed projection).
+ *                Rows that start on 16-byte boundaries are read 16 bytes at a
+ *                time, others element by element.
+ * q_out        : bf16 [T, Hq, 128] contiguous, 16-byte aligned.  It may be q
+ *                itself when q is contiguous (q_tok_stride == Hq*128); otherwise
+ *                it must not overlap q, k, v or the pools.
+ * positions    : int32 [T]; cos_sin: fp32 [max_positions, rotary_dim], 16-byte
+ *                aligned.  rotary_dim is a multiple of 16 in [0, 128]; 0 rotates
+ *                nothing and reads neither.
+ * q_weight, k_weight : fp32 [128], 16-byte aligned, or NULL.  eps >= 0, finite.
+ * A position outside [0, max_positions) leaves that token unwritten (q_out and
+ * its slot), a slot past the pool leaves its K/V unwritten; both are reported as
+ * PKV_ERR_DEVICE_INDEX through pkv_get_device_error().
+ * Returns PKV_OK, PKV_ERR_ARG, PKV_ERR_SHAPE or PKV_ERR_LAUNCH.  T == 0 is a
+ * no-op. */
+int kv_cache_store_norm_rope(void* q_out, const void* q, const void* k, const void* v,
+                             int64_t q_tok_stride, int64_t k_tok_stride, int64_t v_tok_stride,
+                             void* k_cache, void* v_cache, const int32_t* slot_mapping,
+                             const int32_t* positions, const float* cos_sin,
+                             int64_t max_positions, int rotary_dim, int interleaved,
+                             const float* q_weight, const float* k_weight, float eps, int64_t T,
+                             int Hq, int Hkv, int D, int block_size, int64_t num_blocks,
+                             pkv_stream_t stream);
+
+/* kv_cache_store_norm_rope_fp8 — the same into E4M3 pools: the fp32 key value y
+ * is stored as the code nearest to fp32(y * fp32(1 / k_scale)), the value v as
+ * that of fp32(v * fp32(1 / v_scale)), with kv_cache_store_fp8's rounding and
+ * saturation (the key is rounded once, from fp32).  k_scale and v_scale finite
+ * and > 0. */
+int kv_cache_store_norm_rope_fp8(void* q_out, const void* q, const void* k, const void* v,
+                                 int64_t q_tok_stride, int64_t k_tok_stride,
+                                 int64_t v_tok_stride, void* k_cache, void* v_cache,
+                                 const int32_t* slot_mapping, const int32_t* positions,
+                                 const float* cos_sin, int64_t max_positions, int rotary_dim,
+                                 int interleaved, const float* q_weight, const float* k_weight,
+                                 float eps, int64_t T, int Hq, int Hkv, int D, int block_size,
+                                 int64_t num_blocks, float k_scale, float v_scale,
+                                 pkv_stream_t stream);
+
+/* pkv_score_options — what the *_scored attention calls do to a score before
+ * the softmax, and which keys a query sees.  The struct is read during the call
+ * (host memory); the arrays it points to are device memory, read by the
+ * kernels.  For a query at position i of its sequence (decode: context_lens[b]
+ * - 1; prefill row r: Lk - Lq + r), query head h and key j:
+ *   s = scale * <q, K_j>
+ *   softcap > 0          : s = softcap * tanh(s / softcap)
+ *   alibi_slopes != NULL : s = s - alibi_slopes[h] * |i - j|      (fp32 [Hq])
+ * and key j takes part if first <= j <= last, where
+ *   first = max(0, i - window + 1 if window > 0, first_keys[row] if not NULL)
+ *   last  = max(i, prefix_lens[b] - 1 if not NULL)
+ *   window      : a query sees at most the last `window` keys up to itself (0:
+ *                 no limit).
+ *   first_keys  : int32, one per query row (decode [B], prefill [sum Lq]): the
+ *                 first key of the row's own document; documents packed into one
+ *                 sequence then do not see one another.  Any value; below 0
+ *                 counts as 0, past `last` leaves the row without keys.
+ *   prefix_lens : int32 [B], prefill only (NULL for decode): the first
+ *                 prefix_lens[b] tokens of sequence b are visible to every row,
+ *                 so rows inside that prefix see it in both directions.
+ * A row without keys gives out = 0 and lse = -inf.  Keys that no row of a call
+ * sees are never read through a table entry that no visible key shares, and
+ * their contents (infinities and NaN included) do not matter; a key that some
+ * row of its sequence sees must hold finite values.
+ * All zero (or a NULL struct) is plain attention. */
+typedef struct pkv_score_options {
+  float softcap;             /* 0: none; finite, >= 0 */
+  int32_t window;            /* 0: none; >= 0 */
+  const float* alibi_slopes;
+  const int32_t* first_keys;
+  const int32_t* prefix_lens;
+} pkv_score_options;
+
+/* paged_decode_attention_scored — paged_decode_attention under
+ * pkv_score_options.  Only the blocks that hold visible keys are read, so table
+ * entries below them may be stale (blocks freed behind a window).  scale must be
+ * finite and > 0, out must not overlap q, and the workspace size comes from
+ * paged_decode_scored_workspace_bytes with the same arguments; everything else
+ * as paged_decode_attention. */
+size_t paged_decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks_per_seq,
+                                           int block_size, int window, int num_splits);
+int paged_decode_attention_scored(void* out, float* lse, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables,
+                                  int max_blocks_per_seq, const int32_t* context_lens, int B,
+                                  int Hq, int Hkv, int D, int block_size, int64_t num_blocks,
+                                  float scale, const pkv_score_options* options, void* workspace,
+                                  size_t workspace_bytes, int num_splits, pkv_stream_t stream);
+
+/* paged_decode_attention_scored_fp8 — the same over E4M3 pools (key j is code
+ * value * k_scale, value j is code value * v_scale; both scales finite, > 0). */
+int paged_decode_attention_scored_fp8(void* out, float* lse, const void* q, const void* k_cache,
+                                      const void* v_cache, const int32_t* block_tables,
+                                      int max_blocks_per_seq, const int32_t* context_lens, int B,
+                                      int Hq, int Hkv, int D, int block_size, int64_t num_blocks,
+                                      float scale, float k_scale, float v_scale,
+                                      const pkv_score_options* options, void* workspace,
+                                      size_t workspace_bytes, int num_splits,
+                                      pkv_stream_t stream);
+
+/* paged_prefill_attention_scored — paged_prefill_attention under
+ * pkv_score_options.  scale must be finite and > 0 and out must not overlap q.
+ * q and out hold total_q rows (lse and first_keys as well).  A sequence whose
+ * cu_seqlens_q range leaves [0, total_q), or whose prefix_lens[b] is outside
+ * [0, Lk], is reported as PKV_ERR_DEVICE_INDEX and its rows are left unwritten;
+ * everything else as paged_prefill_attention. */
+int paged_prefill_attention_scored(void* out, float* lse, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_tables,
+                                   int max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                                   const int32_t* cu_seqlens_k, int B, int64_t total_q,
+                                   int max_seqlen_q, int max_seqlen_k, int Hq, int Hkv, int D,
+                                   int block_size, int64_t num_blocks, float scale,
+                                   const pkv_score_options* options, pkv_stream_t stream);
 
 /* pkv_get_device_error — synchronises `stream`, then reads and clears the
  * device error word of the current device.  Returns PKV_OK, the first error

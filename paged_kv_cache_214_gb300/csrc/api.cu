@@ -506,6 +506,178 @@ extern "C" int paged_prefill_attention(void* out, float* lse, const void* q, con
   return launch_prefill(a, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+bool aligned_to(const void* p, unsigned n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Whether the byte ranges [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an && bn && x < y + bn && y < x + an;
+}
+
+// Checks and launch shared by the two store entry points.
+int norm_rope_entry(NormRopeArgs a, int64_t max_positions, int D, int block_size,
+                    int64_t num_blocks, pkv_stream_t stream) {
+  if (a.T < 0 || a.Hq <= 0 || !std::isfinite(a.eps) || a.eps < 0.f) return PKV_ERR_ARG;
+  int st = check_pool(a.Hkv, D, block_size, num_blocks);
+  if (st) return st;
+  if (a.rotary_dim < 0 || a.rotary_dim > kHeadDim || a.rotary_dim % 16) return PKV_ERR_SHAPE;
+  if (a.rotary_dim && (max_positions < 0 || max_positions > INT32_MAX)) return PKV_ERR_ARG;
+  if (static_cast<int64_t>(a.Hq) + 2 * static_cast<int64_t>(a.Hkv) > (1 << 20)) return PKV_ERR_SHAPE;
+  if (a.T == 0) return PKV_OK;
+  if (!a.q_out || !a.q || !a.k || !a.v || !a.k_cache || !a.v_cache || !a.slot_mapping)
+    return PKV_ERR_ARG;
+  if (a.rotary_dim && (!a.positions || !a.cos_sin)) return PKV_ERR_ARG;
+  const int64_t q_row = static_cast<int64_t>(a.Hq) * D, kv_row = static_cast<int64_t>(a.Hkv) * D;
+  if (a.q_tok_stride < q_row || a.k_tok_stride < kv_row || a.v_tok_stride < kv_row)
+    return PKV_ERR_ARG;
+  if (!aligned16(a.q_out) || !aligned16(a.k_cache) || !aligned16(a.v_cache)) return PKV_ERR_ARG;
+  if (!aligned16(a.q_weight) || !aligned16(a.k_weight)) return PKV_ERR_ARG;
+  if (a.rotary_dim && !aligned16(a.cos_sin)) return PKV_ERR_ARG;
+  // q_out: q itself, row for row, or memory of its own (a row of it is written
+  // while other rows are still to be read)
+  const uint64_t out_bytes = 2 * static_cast<uint64_t>(a.T) * q_row;
+  const bool in_place = a.q_out == a.q && a.q_tok_stride == q_row;
+  const auto span = [&](int64_t stride, int64_t row) {
+    return 2 * (static_cast<uint64_t>(a.T - 1) * stride + row);
+  };
+  if (!in_place && overlap(a.q_out, out_bytes, a.q, span(a.q_tok_stride, q_row))) return PKV_ERR_ARG;
+  if (overlap(a.q_out, out_bytes, a.k, span(a.k_tok_stride, kv_row)) ||
+      overlap(a.q_out, out_bytes, a.v, span(a.v_tok_stride, kv_row)))
+    return PKV_ERR_ARG;
+  const uint64_t pool = static_cast<uint64_t>(num_blocks) * block_size * kv_row * (a.fp8 ? 1 : 2);
+  if (overlap(a.q_out, out_bytes, a.k_cache, pool) || overlap(a.q_out, out_bytes, a.v_cache, pool))
+    return PKV_ERR_ARG;
+  unsigned* err = device_error_word();
+  if (!err) return PKV_ERR_LAUNCH;
+  a.max_positions = static_cast<int>(a.rotary_dim ? max_positions : 0);
+  a.num_slots = num_blocks * block_size;
+  return launch_norm_rope(a, err, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// pkv_score_options as a call may pass them.
+int check_score_options(const pkv_score_options& o, float scale, bool decode) {
+  if (!std::isfinite(scale) || scale <= 0.f) return PKV_ERR_ARG;
+  if (!std::isfinite(o.softcap) || o.softcap < 0.f || o.window < 0) return PKV_ERR_ARG;
+  if (decode && o.prefix_lens) return PKV_ERR_ARG;
+  if (!aligned_to(o.alibi_slopes, 4) || !aligned_to(o.first_keys, 4) ||
+      !aligned_to(o.prefix_lens, 4))
+    return PKV_ERR_ARG;
+  return PKV_OK;
+}
+
+int decode_scored_entry(const DecodeArgs& a, const pkv_score_options* options, int D,
+                        int block_size, pkv_stream_t stream) {
+  const pkv_score_options opt = options ? *options : pkv_score_options{};
+  int st = check_score_options(opt, a.scale, true);
+  if (st) return st;
+  st = check_decode_args(a, D, block_size);
+  if (st || a.B == 0) return st;
+  const uint64_t bytes = 2ull * a.B * a.Hq * kHeadDim;
+  if (overlap(a.out, bytes, a.q, bytes)) return PKV_ERR_ARG;
+  unsigned* err = device_error_word();
+  if (!err) return PKV_ERR_LAUNCH;
+  const ScoredRowsArgs r{a.out, a.lse, a.q, a.k_cache, a.v_cache, a.block_tables,
+                         a.max_blocks_per_seq, a.context_lens, nullptr, nullptr, a.B, 1, 0, a.Hq,
+                         a.Hkv, a.B, a.num_blocks, a.scale, a.fp8, a.k_scale, a.v_scale, opt};
+  return launch_scored_rows(r, err, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" int kv_cache_store_norm_rope(
+    void* q_out, const void* q, const void* k, const void* v, int64_t q_tok_stride,
+    int64_t k_tok_stride, int64_t v_tok_stride, void* k_cache, void* v_cache,
+    const int32_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int64_t max_positions, int rotary_dim, int interleaved, const float* q_weight,
+    const float* k_weight, float eps, int64_t T, int Hq, int Hkv, int D, int block_size,
+    int64_t num_blocks, pkv_stream_t stream) {
+  const NormRopeArgs a{q_out, q, k, v, q_tok_stride, k_tok_stride, v_tok_stride, k_cache, v_cache,
+                       slot_mapping, positions, cos_sin, 0, rotary_dim, interleaved, q_weight,
+                       k_weight, eps, T, Hq, Hkv, 0, 0, 1.f, 1.f};
+  return norm_rope_entry(a, max_positions, D, block_size, num_blocks, stream);
+}
+
+extern "C" int kv_cache_store_norm_rope_fp8(
+    void* q_out, const void* q, const void* k, const void* v, int64_t q_tok_stride,
+    int64_t k_tok_stride, int64_t v_tok_stride, void* k_cache, void* v_cache,
+    const int32_t* slot_mapping, const int32_t* positions, const float* cos_sin,
+    int64_t max_positions, int rotary_dim, int interleaved, const float* q_weight,
+    const float* k_weight, float eps, int64_t T, int Hq, int Hkv, int D, int block_size,
+    int64_t num_blocks, float k_scale, float v_scale, pkv_stream_t stream) {
+  if (!valid_scale(k_scale) || !valid_scale(v_scale)) return PKV_ERR_ARG;
+  const NormRopeArgs a{q_out, q, k, v, q_tok_stride, k_tok_stride, v_tok_stride, k_cache, v_cache,
+                       slot_mapping, positions, cos_sin, 0, rotary_dim, interleaved, q_weight,
+                       k_weight, eps, T, Hq, Hkv, 0, 1, 1.0f / k_scale, 1.0f / v_scale};
+  return norm_rope_entry(a, max_positions, D, block_size, num_blocks, stream);
+}
+
+extern "C" size_t paged_decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D,
+                                                      int max_blocks_per_seq, int block_size,
+                                                      int window, int num_splits) {
+  (void)B, (void)Hq, (void)Hkv, (void)D, (void)max_blocks_per_seq, (void)block_size;
+  (void)window, (void)num_splits;
+  return 0;
+}
+
+extern "C" int paged_decode_attention_scored(
+    void* out, float* lse, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int B,
+    int Hq, int Hkv, int D, int block_size, int64_t num_blocks, float scale,
+    const pkv_score_options* options, void* workspace, size_t workspace_bytes, int num_splits,
+    pkv_stream_t stream) {
+  const DecodeArgs a{out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                     context_lens, B, Hq, Hkv, num_blocks, scale, workspace, workspace_bytes,
+                     num_splits, 0};
+  return decode_scored_entry(a, options, D, block_size, stream);
+}
+
+extern "C" int paged_decode_attention_scored_fp8(
+    void* out, float* lse, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int B,
+    int Hq, int Hkv, int D, int block_size, int64_t num_blocks, float scale, float k_scale,
+    float v_scale, const pkv_score_options* options, void* workspace, size_t workspace_bytes,
+    int num_splits, pkv_stream_t stream) {
+  const DecodeArgs a{out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                     context_lens, B, Hq, Hkv, num_blocks, scale, workspace, workspace_bytes,
+                     num_splits, 0, 1, 1, k_scale, v_scale};
+  return decode_scored_entry(a, options, D, block_size, stream);
+}
+
+extern "C" int paged_prefill_attention_scored(
+    void* out, float* lse, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* cu_seqlens_q,
+    const int32_t* cu_seqlens_k, int B, int64_t total_q, int max_seqlen_q, int max_seqlen_k,
+    int Hq, int Hkv, int D, int block_size, int64_t num_blocks, float scale,
+    const pkv_score_options* options, pkv_stream_t stream) {
+  const pkv_score_options opt = options ? *options : pkv_score_options{};
+  int st = check_score_options(opt, scale, false);
+  if (st) return st;
+  if (B < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || Hq <= 0 ||
+      max_blocks_per_seq < 0)
+    return PKV_ERR_ARG;
+  st = check_pool(Hkv, D, block_size, num_blocks);
+  if (st) return st;
+  if (Hq % Hkv || total_q > INT32_MAX) return PKV_ERR_SHAPE;
+  if (B == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !cu_seqlens_q || !cu_seqlens_k) return PKV_ERR_ARG;
+  if (max_blocks_per_seq > 0 && !block_tables) return PKV_ERR_ARG;
+  if (num_blocks == 0 && max_blocks_per_seq > 0) return PKV_ERR_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PKV_ERR_ARG;
+  if (static_cast<int64_t>(max_seqlen_k) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
+    return PKV_ERR_ARG;
+  const uint64_t bytes = 2ull * total_q * Hq * kHeadDim;
+  if (overlap(out, bytes, q, bytes)) return PKV_ERR_ARG;
+  unsigned* err = device_error_word();
+  if (!err) return PKV_ERR_LAUNCH;
+  const ScoredRowsArgs r{out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq, nullptr,
+                         cu_seqlens_q, cu_seqlens_k, B, max_seqlen_q, max_seqlen_k, Hq, Hkv,
+                         total_q, num_blocks, scale, 0, 1.f, 1.f, opt};
+  return launch_scored_rows(r, err, reinterpret_cast<cudaStream_t>(stream));
+}
+
 extern "C" int pkv_get_device_error(pkv_stream_t stream) {
   if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return PKV_ERR_LAUNCH;

@@ -53,6 +53,30 @@ int launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const i
                        int n_pairs, int64_t block_bytes, int64_t num_blocks, unsigned* err,
                        cudaStream_t stream);
 
+// Norm of the query and key heads, rotation and store (kv_cache_store_norm_rope).
+struct NormRopeArgs {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_tok_stride, k_tok_stride, v_tok_stride;   // elements
+  void* k_cache;
+  void* v_cache;
+  const int32_t* slot_mapping;
+  const int32_t* positions;
+  const float* cos_sin;
+  int max_positions, rotary_dim, interleaved;
+  const float* q_weight;
+  const float* k_weight;
+  float eps;
+  int64_t T;
+  int Hq, Hkv;
+  int64_t num_slots;
+  int fp8;
+  float k_inv, v_inv;   // E4M3 pools: 1/scale rounded to fp32
+};
+int launch_norm_rope(const NormRopeArgs& a, unsigned* err, cudaStream_t stream);
+
 struct DecodeArgs {
   void* out;
   float* lse;
@@ -146,6 +170,28 @@ struct PrefillArgs {
   float scale;
 };
 int launch_prefill(const PrefillArgs& a, unsigned* err, cudaStream_t stream);
+
+// Scored attention, one warp per (row, head): decode (context_lens; max_q = 1)
+// or prefill (cu_seqlens).
+struct ScoredRowsArgs {
+  void* out;
+  float* lse;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  int max_blocks_per_seq;
+  const int32_t* context_lens;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  int B, max_q, max_k, Hq, Hkv;
+  int64_t total_q, num_blocks;
+  float scale;
+  int fp8;
+  float k_scale, v_scale;
+  pkv_score_options opt;
+};
+int launch_scored_rows(const ScoredRowsArgs& a, unsigned* err, cudaStream_t stream);
 
 // q_len new positions per sequence (speculative verify) on the tensor-core
 // kernel: one item per (sequence, kv head) holding its g*q_len (position, head)

@@ -31,6 +31,15 @@ PKV_DECODE_METADATA_READY = 1
 _lock = threading.Lock()
 _lib = None
 _workspaces = {}
+_stream_workspaces = {}
+
+
+class ScoreOptions(ctypes.Structure):
+    """pkv_score_options of include/pkv.h."""
+
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("alibi_slopes", ctypes.c_void_p), ("first_keys", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
 
 
 class PkvError(RuntimeError):
@@ -98,6 +107,23 @@ def load_library(path: str = LIB_PATH):
         lib.paged_prefill_attention.argtypes = [P, P, P, P, P, P, i32, P, P, i32, i32, i32,
                                                 i32, i32, i32, i32, i64, f32, P]
         lib.paged_prefill_attention.restype = i32
+        opt = ctypes.POINTER(ScoreOptions)
+        store = [P, P, P, P, i64, i64, i64, P, P, P, P, P, i64, i32, i32, P, P, f32, i64, i32,
+                 i32, i32, i32, i64]
+        lib.kv_cache_store_norm_rope.argtypes = [*store, P]
+        lib.kv_cache_store_norm_rope.restype = i32
+        lib.kv_cache_store_norm_rope_fp8.argtypes = [*store, f32, f32, P]
+        lib.kv_cache_store_norm_rope_fp8.restype = i32
+        lib.paged_decode_scored_workspace_bytes.argtypes = [i32] * 8
+        lib.paged_decode_scored_workspace_bytes.restype = sz
+        decode = [P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i64, f32]
+        lib.paged_decode_attention_scored.argtypes = [*decode, opt, P, sz, i32, P]
+        lib.paged_decode_attention_scored.restype = i32
+        lib.paged_decode_attention_scored_fp8.argtypes = [*decode, f32, f32, opt, P, sz, i32, P]
+        lib.paged_decode_attention_scored_fp8.restype = i32
+        lib.paged_prefill_attention_scored.argtypes = [P, P, P, P, P, P, i32, P, P, i32, i64, i32,
+                                                       i32, i32, i32, i32, i32, i64, f32, opt, P]
+        lib.paged_prefill_attention_scored.restype = i32
         lib.pkv_get_device_error.argtypes = [P]
         lib.pkv_get_device_error.restype = i32
         lib.pkv_status_string.argtypes = [i32]
@@ -570,6 +596,324 @@ def paged_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
                                        _ptr(cu_seqlens_k), B, int(max_seqlen_q),
                                        int(max_seqlen_k), Hq, Hkv, D, bs, NB, float(scale),
                                        _stream(stream)), "paged_prefill_attention")
+    return out, lse
+
+
+class _Launch:
+    """Where a call runs: the device of its tensors, made current for the call,
+    and the given stream (a torch stream or a raw handle), or that device's
+    current one.  With a given stream, what the call allocates belongs to it.
+    `handle` is the stream to launch on."""
+
+    __slots__ = ("device", "stream", "handle", "_guards")
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self._guards = device, stream, ()
+
+    def __enter__(self):
+        guards = []
+        if self.device.index != torch.cuda.current_device():
+            guards.append(torch.cuda.device(self.device))
+        if self.stream is not None:
+            s = self.stream
+            if not isinstance(s, torch.cuda.Stream):
+                s = (torch.cuda.ExternalStream(int(s), device=self.device) if int(s)
+                     else torch.cuda.default_stream(self.device))
+            if s.device != self.device:
+                raise ValueError(f"stream is on {s.device}, the tensors on {self.device}")
+            guards.append(torch.cuda.stream(s))
+        for g in guards:
+            g.__enter__()
+        self._guards = tuple(reversed(guards))
+        self.handle = torch.cuda.current_stream().cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        for g in self._guards:
+            g.__exit__(*exc)
+        return False
+
+    def workspace(self, given: Optional[torch.Tensor], nbytes: int):
+        """(pointer, bytes) of the caller's workspace, or of one kept for this
+        stream (calls on one stream do not overlap).  A captured call needs the
+        caller's own: a later, larger call would free the kept one under the
+        graph."""
+        if given is not None:
+            if not isinstance(given, torch.Tensor) or given.device != self.device:
+                raise ValueError(f"workspace must be a tensor on {self.device}")
+            if not given.is_contiguous():
+                raise ValueError("workspace must be contiguous")
+            return given.data_ptr(), given.numel() * given.element_size()
+        if not nbytes:
+            return 0, 0
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("a captured call needs a workspace of its own (zeroed, of "
+                             f"{nbytes} bytes)")
+        key = (self.device.index, self.handle)
+        ws = _stream_workspaces.get(key)
+        if ws is None or ws.numel() < nbytes:
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            _stream_workspaces[key] = ws
+        return ws.data_ptr(), ws.numel()
+
+
+def _same_device(device: torch.device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor, fp8: bool):
+    NB, bs, Hkv, D = (_fp8_pool_dims if fp8 else _pool_dims)(k_cache, v_cache)
+    return NB, bs, Hkv, D
+
+
+def _norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                     k_weight, eps, interleaved, q_out, stream, scales):
+    fp8 = scales is not None
+    lib = load_library()
+    NB, bs, Hkv, D = _pools(k_cache, v_cache, fp8)
+    _need(q, "q", torch.bfloat16, 3, contiguous=False)
+    T, Hq = q.shape[0], q.shape[1]
+    for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        _need(t, name, torch.bfloat16, 3, contiguous=False)
+        if t.shape[0] != T or t.shape[1] != heads or t.shape[2] != D:
+            raise ValueError(f"{name} must be [{T}, {heads}, {D}], got {tuple(t.shape)}")
+        if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
+            raise ValueError(f"{name} must have contiguous rows")
+    _need(slot_mapping, "slot_mapping", torch.int32, 1)
+    if slot_mapping.shape[0] != T:
+        raise ValueError("slot_mapping and q disagree on T")
+    rotary = places = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32, 2)
+        places, rotary = cos_sin.shape
+        _need(positions, "positions", torch.int32, 1)
+        if positions.shape[0] != T:
+            raise ValueError("positions and q disagree on T")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _need(t, name, torch.float32, 1)
+            if t.shape[0] != D:
+                raise ValueError(f"{name} must be [{D}]")
+    if q_out is not None:
+        _need(q_out, "q_out", torch.bfloat16, 3)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out and q differ in shape")
+    _same_device(k_cache.device, q=q, k=k, v=v, v_cache=v_cache, slot_mapping=slot_mapping,
+                 positions=positions if rotary else None, cos_sin=cos_sin, q_weight=q_weight,
+                 k_weight=k_weight, q_out=q_out)
+    with _Launch(k_cache.device, stream) as at:
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=at.device)
+        # a single row's token stride says nothing (torch may give it any value)
+        strides = [t.stride(0) if T > 1 else t.shape[1] * D for t in (q, k, v)]
+        args = (q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
+                k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+                positions.data_ptr() if rotary else None,
+                cos_sin.data_ptr() if rotary else None, places, rotary, 1 if interleaved else 0,
+                None if q_weight is None else q_weight.data_ptr(),
+                None if k_weight is None else k_weight.data_ptr(), eps, T, Hq, Hkv, D, bs, NB)
+        if fp8:
+            _check(lib.kv_cache_store_norm_rope_fp8(*args, scales[0], scales[1], at.handle),
+                   "kv_cache_store_norm_rope_fp8")
+        else:
+            _check(lib.kv_cache_store_norm_rope(*args, at.handle), "kv_cache_store_norm_rope")
+    return q_out
+
+
+def kv_cache_store_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             k_cache: torch.Tensor, v_cache: torch.Tensor,
+                             slot_mapping: torch.Tensor, positions: Optional[torch.Tensor],
+                             cos_sin: Optional[torch.Tensor],
+                             q_weight: Optional[torch.Tensor] = None,
+                             k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                             interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                             stream=None) -> torch.Tensor:
+    """RMS norm of every query and key head, rotation by position, and the store
+    of K/V, in one launch.  q bf16 [T, Hq, D], k / v bf16 [T, Hkv, D] (token
+    stride free: slices of one packed projection will do); positions int32 [T];
+    cos_sin fp32 [max_positions, R]: R/2 cosines, then R/2 sines (None: no
+    rotation); q_weight / k_weight fp32 [D] (None: that tensor is not normed).
+    Returns the queries, bf16 [T, Hq, D] (q_out; it may be q if q is
+    contiguous)."""
+    return _norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                            k_weight, eps, interleaved, q_out, stream, None)
+
+
+def kv_cache_store_norm_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                 k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 slot_mapping: torch.Tensor, positions: Optional[torch.Tensor],
+                                 cos_sin: Optional[torch.Tensor], k_scale: float, v_scale: float,
+                                 q_weight: Optional[torch.Tensor] = None,
+                                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """kv_cache_store_norm_rope into uint8 E4M3 pools (one scale per tensor)."""
+    return _norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                            k_weight, eps, interleaved, q_out, stream, (k_scale, v_scale))
+
+
+def _score_options(rows: int, batch: int, Hq: int, softcap, alibi_slopes, window, first_keys,
+                   prefix_lens=None) -> ScoreOptions:
+    o = ScoreOptions(softcap, window)
+    if alibi_slopes is not None:
+        _need(alibi_slopes, "alibi_slopes", torch.float32, 1)
+        if alibi_slopes.shape[0] != Hq:
+            raise ValueError(f"alibi_slopes must be [{Hq}]")
+        o.alibi_slopes = alibi_slopes.data_ptr()
+    if first_keys is not None:
+        _need(first_keys, "first_keys", torch.int32, 1)
+        if first_keys.shape[0] != rows:
+            raise ValueError(f"first_keys must be [{rows}]")
+        o.first_keys = first_keys.data_ptr()
+    if prefix_lens is not None:
+        _need(prefix_lens, "prefix_lens", torch.int32, 1)
+        if prefix_lens.shape[0] != batch:
+            raise ValueError(f"prefix_lens must be [{batch}]")
+        o.prefix_lens = prefix_lens.data_ptr()
+    return o
+
+
+def _outputs(q: torch.Tensor, out, lse, want_lse: bool):
+    """Checks of a given out / lse, before anything is allocated."""
+    if out is not None:
+        _need(out, "out", torch.bfloat16, 3)
+        if out.shape != q.shape:
+            raise ValueError("out and q differ in shape")
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+        if lse.shape != q.shape[:2]:
+            raise ValueError(f"lse must be {tuple(q.shape[:2])}")
+
+
+def paged_decode_scored_workspace_bytes(B: int, Hq: int, Hkv: int, D: int,
+                                        max_blocks_per_seq: int, block_size: int = 256,
+                                        window: int = 0, num_splits: int = 0) -> int:
+    return int(load_library().paged_decode_scored_workspace_bytes(
+        B, Hq, Hkv, D, max_blocks_per_seq, block_size, window, num_splits))
+
+
+def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scales, softcap,
+                   alibi_slopes, window, first_keys, out, lse, workspace, num_splits, want_lse,
+                   stream):
+    fp8 = scales is not None
+    lib = load_library()
+    NB, bs, Hkv, D = _pools(k_cache, v_cache, fp8)
+    _need(q, "q", torch.bfloat16, 3)
+    B, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q head_dim differs from the cache's")
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    maxblk = block_tables.shape[1]
+    if block_tables.shape[0] != B or context_lens.shape[0] != B:
+        raise ValueError("block_tables / context_lens batch differs from q")
+    options = _score_options(B, B, Hq, softcap, alibi_slopes, window, first_keys)
+    _outputs(q, out, lse, want_lse)
+    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 context_lens=context_lens, alibi_slopes=alibi_slopes, first_keys=first_keys,
+                 out=out, lse=lse)
+    with _Launch(q.device, stream) as at:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=at.device)
+        need = lib.paged_decode_scored_workspace_bytes(B, Hq, Hkv, D, maxblk, bs, window,
+                                                       num_splits)
+        ws, ws_bytes = at.workspace(workspace, need)
+        args = (out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
+                k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), maxblk,
+                context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, scale)
+        if fp8:
+            _check(lib.paged_decode_attention_scored_fp8(
+                *args, scales[0], scales[1], options, ws, ws_bytes, num_splits, at.handle),
+                "paged_decode_attention_scored_fp8")
+        else:
+            _check(lib.paged_decode_attention_scored(*args, options, ws, ws_bytes, num_splits,
+                                                     at.handle), "paged_decode_attention_scored")
+    return out, lse
+
+
+def paged_decode_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                  scale: float, softcap: float = 0.0,
+                                  alibi_slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                  first_keys: Optional[torch.Tensor] = None,
+                                  out: Optional[torch.Tensor] = None,
+                                  lse: Optional[torch.Tensor] = None,
+                                  workspace: Optional[torch.Tensor] = None, num_splits: int = 0,
+                                  want_lse: bool = True, stream=None
+                                  ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """paged_decode_attention with scores capped by softcap * tanh(s / softcap),
+    biased by -alibi_slopes[h] * distance (fp32 [Hq]), and restricted to the last
+    `window` keys and to keys from first_keys[b] on (int32 [B]).  Returns (out
+    bf16 [B, Hq, D], lse fp32 [B, Hq] or None).  Without a given workspace one is
+    kept per stream; a captured call needs its own."""
+    return _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, None, softcap,
+                          alibi_slopes, window, first_keys, out, lse, workspace, num_splits,
+                          want_lse, stream)
+
+
+def paged_decode_attention_scored_fp8(q: torch.Tensor, k_cache: torch.Tensor,
+                                      v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                      context_lens: torch.Tensor, scale: float, k_scale: float,
+                                      v_scale: float, softcap: float = 0.0,
+                                      alibi_slopes: Optional[torch.Tensor] = None,
+                                      window: int = 0, first_keys: Optional[torch.Tensor] = None,
+                                      out: Optional[torch.Tensor] = None,
+                                      lse: Optional[torch.Tensor] = None,
+                                      workspace: Optional[torch.Tensor] = None,
+                                      num_splits: int = 0, want_lse: bool = True, stream=None
+                                      ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """paged_decode_attention_scored over uint8 E4M3 pools."""
+    return _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale,
+                          (k_scale, v_scale), softcap, alibi_slopes, window, first_keys, out, lse,
+                          workspace, num_splits, want_lse, stream)
+
+
+def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                                   cu_seqlens_k: torch.Tensor, max_seqlen_q: int,
+                                   max_seqlen_k: int, scale: float, softcap: float = 0.0,
+                                   alibi_slopes: Optional[torch.Tensor] = None, window: int = 0,
+                                   first_keys: Optional[torch.Tensor] = None,
+                                   prefix_lens: Optional[torch.Tensor] = None,
+                                   out: Optional[torch.Tensor] = None,
+                                   lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                                   stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """paged_prefill_attention with the options of paged_decode_attention_scored
+    (first_keys: int32, one per query row) and prefix_lens (int32 [B]): the first
+    prefix_lens[b] tokens are visible to every row of sequence b.  Returns (out
+    bf16 [sum Lq, Hq, D], lse fp32 [sum Lq, Hq] or None)."""
+    lib = load_library()
+    NB, bs, Hkv, D = _pool_dims(k_cache, v_cache)
+    _need(q, "q", torch.bfloat16, 3)
+    Nq, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError("q head_dim differs from the cache's")
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    B = cu_seqlens_q.shape[0] - 1
+    if B < 0 or cu_seqlens_k.shape[0] != B + 1 or block_tables.shape[0] != B:
+        raise ValueError("cu_seqlens / block_tables batch sizes differ")
+    options = _score_options(Nq, B, Hq, softcap, alibi_slopes, window, first_keys, prefix_lens)
+    _outputs(q, out, lse, want_lse)
+    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, alibi_slopes=alibi_slopes,
+                 first_keys=first_keys, prefix_lens=prefix_lens, out=out, lse=lse)
+    with _Launch(q.device, stream) as at:
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and want_lse:
+            lse = torch.empty((Nq, Hq), dtype=torch.float32, device=at.device)
+        _check(lib.paged_prefill_attention_scored(
+            out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B,
+            Nq, max_seqlen_q, max_seqlen_k, Hq, Hkv, D, bs, NB, scale, options, at.handle),
+            "paged_prefill_attention_scored")
     return out, lse
 
 
