@@ -576,12 +576,16 @@ int decode_scored_entry(const DecodeArgs& a, const pkv_score_options* options, i
   if (st || a.B == 0) return st;
   const uint64_t bytes = 2ull * a.B * a.Hq * kHeadDim;
   if (overlap(a.out, bytes, a.q, bytes)) return PKV_ERR_ARG;
+  DecodePlan plan;
+  st = plan_decode_scored(a.B, a.Hq, a.Hkv, a.max_blocks_per_seq, opt.window, a.num_splits,
+                          device_sm_count(), &plan);
+  if (st) return st;
+  if (plan.workspace_bytes && (!a.workspace || a.workspace_bytes < plan.workspace_bytes ||
+                               !aligned_to(a.workspace, 256)))
+    return PKV_ERR_WORKSPACE;
   unsigned* err = device_error_word();
   if (!err) return PKV_ERR_LAUNCH;
-  const ScoredRowsArgs r{a.out, a.lse, a.q, a.k_cache, a.v_cache, a.block_tables,
-                         a.max_blocks_per_seq, a.context_lens, nullptr, nullptr, a.B, 1, 0, a.Hq,
-                         a.Hkv, a.B, a.num_blocks, a.scale, a.fp8, a.k_scale, a.v_scale, opt};
-  return launch_scored_rows(r, err, reinterpret_cast<cudaStream_t>(stream));
+  return launch_decode_scored(a, opt, plan, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -616,9 +620,12 @@ extern "C" int kv_cache_store_norm_rope_fp8(
 extern "C" size_t paged_decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D,
                                                       int max_blocks_per_seq, int block_size,
                                                       int window, int num_splits) {
-  (void)B, (void)Hq, (void)Hkv, (void)D, (void)max_blocks_per_seq, (void)block_size;
-  (void)window, (void)num_splits;
-  return 0;
+  if (D != kHeadDim || block_size != kBlockSize || num_splits < 0) return 0;
+  DecodePlan plan;
+  if (plan_decode_scored(B, Hq, Hkv, max_blocks_per_seq, window, num_splits, device_sm_count(),
+                         &plan))
+    return 0;
+  return plan.workspace_bytes;
 }
 
 extern "C" int paged_decode_attention_scored(
@@ -702,6 +709,7 @@ extern "C" int pkv_testing_set_wait_fault(int64_t wait_limit_ns, int withhold_ti
   const unsigned long long lim = static_cast<unsigned long long>(wait_limit_ns);
   const int w = withhold_tile + 1;
   int st = set_wait_hook_decode(lim, w);
+  if (st == PKV_OK) st = set_wait_hook_decode_scored(lim, w);
   if (st == PKV_OK) st = set_wait_hook_prefill(lim, w);
   return st;
 }

@@ -1,0 +1,79 @@
+// decode_scored.cu — paged decode attention whose scores are capped or biased by
+// distance and whose keys may start at a window's or a document's first one
+// (pkv_score_options), on the split-K kernel of decode_kernel.cuh.
+//
+// What the options add to that kernel.  Per score: the cap, two special-function
+// operations (modified_score), and one multiply-add of the distance; both work
+// in log2 units.  Per block: the first key comes from the context length, so
+// with a window or documents a block's page ids are read after it (one more
+// dependent load).  Ranges start at the first key's block and the ring at its
+// 64-token tile, so a window costs the bytes of the window, and pages behind it
+// are never read.  The grid covers the blocks a window can touch, not the
+// table's.  Bound by HBM as the plain decode is: a capped score's arithmetic
+// hides under the copies.
+
+#include "decode_kernel.cuh"
+
+namespace pkv {
+
+int set_wait_hook_decode_scored(unsigned long long limit_ns, int withhold_plus1) {
+  const WaitHook h{limit_ns, withhold_plus1, 0};
+  return cudaMemcpyToSymbol(g_wait_hook, &h, sizeof h) == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
+}
+
+int plan_decode_scored(int B, int Hq, int Hkv, int max_blocks_per_seq, int window, int num_splits,
+                       int sm_count, DecodePlan* plan) {
+  if (B < 0 || window < 0 || max_blocks_per_seq < 0) return PKV_ERR_ARG;
+  int blocks = max_blocks_per_seq;
+  if (window > 0) {
+    // the window's tokens and up to a block before them
+    const int64_t touched = (static_cast<int64_t>(window) + 2 * kBlockSize - 2) / kBlockSize;
+    if (touched < blocks) blocks = static_cast<int>(touched);
+  }
+  const int st = plan_decode(B, Hq, Hkv, blocks, num_splits, sm_count, 0, plan);
+  if (st) return st;
+  // the launch grid: (splits, kv heads x head groups, sequences)
+  if (B > 65535 || static_cast<int64_t>(Hkv) * plan->head_groups > 65535) return PKV_ERR_SHAPE;
+  return PKV_OK;
+}
+
+namespace {
+
+template <int G>
+int launch_form(const DecodeArgs& a, const DecodePlan& plan, const DecodeParams& prm,
+                const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t stream) {
+  // the forms and the rules between them are the plain decode's (launch_decode)
+  if (a.fp8)
+    return plan.split_tokens >= 8 * kBlockSize
+               ? launch_g<G, false, true, true, 1, true>(a, plan, prm, km, vm, stream)
+               : launch_g<G, false, true, false, 1, true>(a, plan, prm, km, vm, stream);
+  if (plan.consumer_groups == 2)
+    return launch_g<G, false, false, true, 2, true>(a, plan, prm, km, vm, stream);
+  if (plan.split_tokens < kBlockSize)
+    return launch_g<G, false, false, false, 1, true>(a, plan, prm, km, vm, stream);
+  return launch_g<G, false, false, true, 1, true>(a, plan, prm, km, vm, stream);
+}
+
+}  // namespace
+
+int launch_decode_scored(const DecodeArgs& a, const pkv_score_options& opt, const DecodePlan& plan,
+                         unsigned* err, cudaStream_t stream) {
+  CUtensorMap km, vm;
+  if (!decode_maps(a, &km, &vm)) return PKV_ERR_ARG;
+  DecodeParams prm = decode_params(a, plan, err);
+  if (opt.softcap > 0.f) {
+    prm.cap_log2 = opt.softcap * 1.4426950408889634f;
+    prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
+  }
+  prm.window = opt.window;
+  prm.slopes = opt.alibi_slopes;
+  prm.first_keys = opt.first_keys;
+  switch (plan.heads_per_cta) {
+    case 8: return launch_form<8>(a, plan, prm, km, vm, stream);
+    case 4: return launch_form<4>(a, plan, prm, km, vm, stream);
+    case 2: return launch_form<2>(a, plan, prm, km, vm, stream);
+    default: return launch_form<1>(a, plan, prm, km, vm, stream);
+  }
+}
+
+}  // namespace pkv

@@ -131,6 +131,12 @@ struct DecodePlan {
 int plan_decode(int B, int Hq, int Hkv, int max_blocks_per_seq, int num_splits,
                 int sm_count, int prefix_blocks, DecodePlan* plan);
 
+// The same for scored decode: window > 0 bounds the blocks a sequence needs.
+int plan_decode_scored(int B, int Hq, int Hkv, int max_blocks_per_seq, int window, int num_splits,
+                       int sm_count, DecodePlan* plan);
+int launch_decode_scored(const DecodeArgs& a, const pkv_score_options& opt, const DecodePlan& plan,
+                         unsigned* err, cudaStream_t stream);
+
 // Attention of every (sequence, query head) of the batch over a shared prefix
 // of prefix_tokens tokens (the first blocks of sequence 0's table), as one
 // normalised fp32 partial [B*Hq, 128] plus log2-sum-exp [B*Hq] per row.
@@ -215,6 +221,7 @@ int verify_rows_fit(int g, int q_len);
 // Test hook of the decode / prefill kernels' bounded waits (see
 // pkv_testing_set_wait_fault); 0, 0 turns it off.
 int set_wait_hook_decode(unsigned long long limit_ns, int withhold_plus1);
+int set_wait_hook_decode_scored(unsigned long long limit_ns, int withhold_plus1);
 int set_wait_hook_prefill(unsigned long long limit_ns, int withhold_plus1);
 int launch_verify(const VerifyArgs& a, unsigned* err, cudaStream_t stream);
 
