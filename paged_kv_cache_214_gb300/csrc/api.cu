@@ -679,10 +679,10 @@ extern "C" int paged_prefill_attention_scored(
   if (overlap(out, bytes, q, bytes)) return PKV_ERR_ARG;
   unsigned* err = device_error_word();
   if (!err) return PKV_ERR_LAUNCH;
-  const ScoredRowsArgs r{out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq, nullptr,
-                         cu_seqlens_q, cu_seqlens_k, B, max_seqlen_q, max_seqlen_k, Hq, Hkv,
-                         total_q, num_blocks, scale, 0, 1.f, 1.f, opt};
-  return launch_scored_rows(r, err, reinterpret_cast<cudaStream_t>(stream));
+  const PrefillArgs a{out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                      cu_seqlens_q, cu_seqlens_k, B, max_seqlen_q, max_seqlen_k, Hq, Hkv,
+                      num_blocks, scale};
+  return launch_prefill_scored(a, total_q, opt, err, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int pkv_get_device_error(pkv_stream_t stream) {
@@ -711,6 +711,7 @@ extern "C" int pkv_testing_set_wait_fault(int64_t wait_limit_ns, int withhold_ti
   int st = set_wait_hook_decode(lim, w);
   if (st == PKV_OK) st = set_wait_hook_decode_scored(lim, w);
   if (st == PKV_OK) st = set_wait_hook_prefill(lim, w);
+  if (st == PKV_OK) st = set_wait_hook_prefill_scored(lim, w);
   return st;
 }
 

@@ -131,11 +131,7 @@ struct RowScore {
 // infinity, whose reciprocal is 0).
 __device__ __forceinline__ float modified_score(float x, float qmul, const RowScore& rs, int dist) {
   float v = x * qmul;
-  if (rs.cap > 0.f) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(v)));
-    v = fmaf(-2.f * rs.cap, r, rs.cap);
-  }
+  if (rs.cap > 0.f) v = fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(v)), rs.cap);
   return fmaf(-rs.slope, fabsf(static_cast<float>(dist)), v);
 }
 

@@ -182,6 +182,14 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Reciprocal on the special-function unit (rcp.approx.ftz): within one ulp,
+// 1 / inf = 0.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two bf16 packed in a 32-bit word -> two floats (exact: bf16 is the top half
 // of a binary32).
 __device__ __forceinline__ float bf16lo(uint32_t u) { return __uint_as_float(u << 16); }

@@ -177,27 +177,9 @@ struct PrefillArgs {
 };
 int launch_prefill(const PrefillArgs& a, unsigned* err, cudaStream_t stream);
 
-// Scored attention, one warp per (row, head): decode (context_lens; max_q = 1)
-// or prefill (cu_seqlens).
-struct ScoredRowsArgs {
-  void* out;
-  float* lse;
-  const void* q;
-  const void* k_cache;
-  const void* v_cache;
-  const int32_t* block_tables;
-  int max_blocks_per_seq;
-  const int32_t* context_lens;
-  const int32_t* cu_seqlens_q;
-  const int32_t* cu_seqlens_k;
-  int B, max_q, max_k, Hq, Hkv;
-  int64_t total_q, num_blocks;
-  float scale;
-  int fp8;
-  float k_scale, v_scale;
-  pkv_score_options opt;
-};
-int launch_scored_rows(const ScoredRowsArgs& a, unsigned* err, cudaStream_t stream);
+// The same under pkv_score_options; q and out hold total_q rows.
+int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score_options& opt,
+                          unsigned* err, cudaStream_t stream);
 
 // q_len new positions per sequence (speculative verify) on the tensor-core
 // kernel: one item per (sequence, kv head) holding its g*q_len (position, head)
@@ -223,6 +205,7 @@ int verify_rows_fit(int g, int q_len);
 int set_wait_hook_decode(unsigned long long limit_ns, int withhold_plus1);
 int set_wait_hook_decode_scored(unsigned long long limit_ns, int withhold_plus1);
 int set_wait_hook_prefill(unsigned long long limit_ns, int withhold_plus1);
+int set_wait_hook_prefill_scored(unsigned long long limit_ns, int withhold_plus1);
 int launch_verify(const VerifyArgs& a, unsigned* err, cudaStream_t stream);
 
 }  // namespace pkv
