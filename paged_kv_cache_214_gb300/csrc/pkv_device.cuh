@@ -190,6 +190,18 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// Largest of three, and of |a|, |b|, |c| (one instruction on sm_100 and later).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+  float y;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 // Two bf16 packed in a 32-bit word -> two floats (exact: bf16 is the top half
 // of a binary32).
 __device__ __forceinline__ float bf16lo(uint32_t u) { return __uint_as_float(u << 16); }

@@ -99,6 +99,11 @@ constexpr uint32_t kColO = 384;
 constexpr float kLazyRescale = 8.f;    // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr float kTanhPoly = 0.625f;    // |s / softcap| up to which the cap is a polynomial
+// Registers of a thread in scored mode, where the softmax holds more than the
+// 168 that 384 threads get each: 256 x 200 + 128 x 104 = 384 x 168.
+constexpr int kRegsSoftmax = 200;
+constexpr int kRegsOther = 104;
 
 // Kernel modes.  kCausal: (chunked) prefill, one item per (row tile, sequence,
 // query head).  kPrefixPass: the shared-prefix pass of a decode batch.
@@ -138,7 +143,7 @@ struct PrefillParams {
   // 2 log2(e) / softcap); window (0: none); per-head slopes, per-row first keys
   // and per-sequence two-way prefixes (null: none)
   int64_t total_q;
-  float cap_log2;
+  float cap_log2, cap_x;   // cap_x: scale / softcap
   int window;
   const float* slopes;
   const int32_t* first_keys;
@@ -392,6 +397,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  if (warp >= kSoftmaxWarps) {
+  if constexpr (kMode == kScored)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
   if (warp == kQKWarp) {
     // ------------------------------------------------------------ TMA: Q and K
     // An item's Q goes into the single Q buffer right after its first K tile
@@ -632,8 +640,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       umma_commit_warp(bar(kBarDrainPV));
       (void)warp_wait(bar(kBarDrainPV), 0);
     }
+  }
   } else {
     // ------------------------------------------------------------ softmax
+    if constexpr (kMode == kScored)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // Warp w owns 16 whole rows of every tile: TMEM lanes 32(w%4) + 16(w/4) +
     // [0, 16).  Through the 16x256b access shape thread t holds rows
     // ra = .. + t/4 and rb = ra + 8, key columns 8k + 2(t%4) + {0, 1}
@@ -775,31 +786,90 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         uint32_t r[64];
         tmem_ld16x256_x16_wait(s_col, r);
         const int j0 = (it.kt0 + kt) * kN + 2 * m4;   // key of register 0
+        const int t0 = (it.kt0 + kt) * kN, t1 = t0 + kN - 1;
+        // Scored mode, capped or biased: r becomes the score in log2 units less a
+        // constant of the row and tile, offa / offb.  A bias -slope (i - j) is
+        // slope (j - t0) + slope (t0 - i): the first part is the same for every
+        // row and exact enough (j - t0 < 128), the second is that constant.
+        float offa = 0.f, offb = 0.f;
         if constexpr (kCap || kBias) {
-          // the scores in log2 units: capped as modified_score of the decode
-          // does, c tanh(s / c) = c - 2c / (1 + e^(2 s / c)), then biased
-          const f32x2 one = pack2(1.f, 1.f), cap = pack2(p.cap_log2, p.cap_log2);
-          const f32x2 neg2cap = pack2(-2.f * p.cap_log2, -2.f * p.cap_log2);
-          const float da = static_cast<float>(visa - j0), db = static_cast<float>(visb - j0);
-          auto modify = [&](uint32_t& lo, uint32_t& hi, float dist) {
-            f32x2 v = mul2(pack2(__uint_as_float(lo), __uint_as_float(hi)), sc2);
-            if constexpr (kCap) {
-              v = add2(pack2(ex2(lo2(v)), ex2(hi2(v))), one);
-              v = fma2(pack2(rcp_approx(lo2(v)), rcp_approx(hi2(v))), neg2cap, cap);
+          f32x2 kq = pack2(slope * (2 * m4), slope * (2 * m4 + 1));
+          const f32x2 step = pack2(slope * 8.f, slope * 8.f);
+          auto finish = [&](int q, f32x2 va, f32x2 vb) {
+            if constexpr (kBias) {
+              va = add2(va, kq);
+              vb = add2(vb, kq);
+              kq = add2(kq, step);
             }
-            if constexpr (kBias)
-              v = fma2(pack2(fabsf(dist), fabsf(dist - 1.f)), pack2(-slope, -slope), v);
-            lo = __float_as_uint(lo2(v));
-            hi = __float_as_uint(hi2(v));
+            r[4 * q] = __float_as_uint(lo2(va));
+            r[4 * q + 1] = __float_as_uint(hi2(va));
+            r[4 * q + 2] = __float_as_uint(lo2(vb));
+            r[4 * q + 3] = __float_as_uint(hi2(vb));
           };
+          auto raw = [&](int k) {
+            return pack2(__uint_as_float(r[k]), __uint_as_float(r[k + 1]));
+          };
+          if constexpr (kBias) {
+            offa = slope * static_cast<float>(t0 - visa);
+            offb = slope * static_cast<float>(t0 - visb);
+          }
+          if constexpr (kCap) {
+            float big = 0.f;   // largest |product| of the thread's rows
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            modify(r[4 * q], r[4 * q + 1], da - 8.f * q);
-            modify(r[4 * q + 2], r[4 * q + 3], db - 8.f * q);
+            for (int q = 0; q < 64; q += 2)
+              big = absmax3(big, __uint_as_float(r[q]), __uint_as_float(r[q + 1]));
+            // c tanh(s / c), s / c = x.  While |x| <= 0.625 in the whole warp: an
+            // odd polynomial (minimax for the absolute error, 3e-8, computed by
+            // exchange for this interval), on the FMA pipe.  Else 1 - 2 / (1 + e^2x)
+            // with two special-function operations, which are scarcer.
+            if (__any_sync(kFull, !(big * p.cap_x <= kTanhPoly))) {
+              const f32x2 one = pack2(1.f, 1.f), cap = pack2(p.cap_log2, p.cap_log2);
+              const f32x2 neg2cap = pack2(-2.f * p.cap_log2, -2.f * p.cap_log2);
+              auto exact = [&](f32x2 x) {
+                x = mul2(x, sc2);
+                x = add2(pack2(ex2(lo2(x)), ex2(hi2(x))), one);
+                return fma2(pack2(rcp_approx(lo2(x)), rcp_approx(hi2(x))), neg2cap, cap);
+              };
+#pragma unroll
+              for (int q = 0; q < 16; ++q) finish(q, exact(raw(4 * q)), exact(raw(4 * q + 2)));
+            } else {
+              const f32x2 cx = pack2(p.cap_x, p.cap_x);
+              const float c = p.cap_log2;
+              const f32x2 c0 = pack2(c * 0.999999459f, c * 0.999999459f);
+              const f32x2 c1 = pack2(c * -0.333304827f, c * -0.333304827f);
+              const f32x2 c2 = pack2(c * 0.132910316f, c * 0.132910316f);
+              const f32x2 c3 = pack2(c * -0.0513628685f, c * -0.0513628685f);
+              const f32x2 c4 = pack2(c * 0.0145300686f, c * 0.0145300686f);
+              auto poly = [&](f32x2 x) {
+                x = mul2(x, cx);
+                const f32x2 u = mul2(x, x);
+                return mul2(x, fma2(fma2(fma2(fma2(c4, u, c3), u, c2), u, c1), u, c0));
+              };
+#pragma unroll
+              for (int q = 0; q < 16; ++q) finish(q, poly(raw(4 * q)), poly(raw(4 * q + 2)));
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 16; ++q) finish(q, mul2(raw(4 * q), sc2), mul2(raw(4 * q + 2), sc2));
+          }
+          if constexpr (kBias) {
+            // keys past the row's own position (a two-way prefix) are biased by
+            // slope (i - j) instead: 2 slope (i - j) more
+            if (__any_sync(kFull, (hia > visa && t1 > visa) || (hib > visb && t1 > visb))) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int past = j0 + 8 * q + (e & 1) - (e < 2 ? visa : visb);
+                  if (past > 0)
+                    r[4 * q + e] = __float_as_uint(fmaf(-2.f * slope, static_cast<float>(past),
+                                                        __uint_as_float(r[4 * q + e])));
+                }
+              }
+            }
           }
         }
         if constexpr (kMode == kScored) {
-          const int t0 = (it.kt0 + kt) * kN, t1 = t0 + kN - 1;
           if (__any_sync(kFull, loa > t0 || lob > t0 || hia < t1 || hib < t1)) {
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
@@ -822,6 +892,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         float xa0 = __uint_as_float(r[0]), xa1 = __uint_as_float(r[1]);
         float xb0 = __uint_as_float(r[2]), xb1 = __uint_as_float(r[3]);
+        if constexpr (kMode == kScored) {
+#pragma unroll
+          for (int q = 1; q < 16; ++q) {
+            xa0 = max3(xa0, __uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]));
+            xb0 = max3(xb0, __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          }
+        } else
 #pragma unroll
         for (int q = 1; q < 16; ++q) {
           xa0 = fmaxf(xa0, __uint_as_float(r[4 * q]));
@@ -830,8 +907,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           xb1 = fmaxf(xb1, __uint_as_float(r[4 * q + 3]));
         }
         const float unit = kCap || kBias ? 1.f : p.scale_log2;   // of r, in log2 units
-        const float mta = row_max(fmaxf(xa0, xa1)) * unit;
-        const float mtb = row_max(fmaxf(xb0, xb1)) * unit;
+        const float mta = row_max(fmaxf(xa0, xa1)) * unit + offa;
+        const float mtb = row_max(fmaxf(xb0, xb1)) * unit + offb;
         if (kt == 0) {
           ma = mta;
           mb = mtb;
@@ -872,8 +949,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // 8q + 2 m4 + {0, 1} (the 16x128b shape).  Hidden keys hold -inf and
         // get weight exactly 0.
         // (a row that has seen no key yet: 2^(-inf - 0))
-        const float na = kMode == kScored && ma == -INFINITY ? 0.f : -ma;
-        const float nb = kMode == kScored && mb == -INFINITY ? 0.f : -mb;
+        const float na = kMode == kScored && ma == -INFINITY ? 0.f : offa - ma;
+        const float nb = kMode == kScored && mb == -INFINITY ? 0.f : offb - mb;
         const f32x2 nma = pack2(na, na), nmb = pack2(nb, nb);
         uint32_t pk[32];
         f32x2 sa = pack2(0.f, 0.f), sb2 = pack2(0.f, 0.f);
@@ -972,6 +1049,17 @@ bool set_smem_attr() {
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes) != cudaSuccess)
       return false;
+    if (kMode == kScored) {
+      // the split of the registers must fit what a block is launched with, or its
+      // warps would wait for registers that never come
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, paged_prefill_kernel<kMode, kCap, kBias>) != cudaSuccess)
+        return false;
+      const int launched = (fa.numRegs + 7) / 8 * 8 * kThreads;
+      if (32 * (kSoftmaxWarps * kRegsSoftmax + (kThreads / 32 - kSoftmaxWarps) * kRegsOther) >
+          launched)
+        return false;
+    }
     attr_set[dev] = true;
   }
   return true;

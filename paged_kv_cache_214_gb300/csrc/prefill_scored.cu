@@ -60,6 +60,7 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   prm.prefix_lens = opt.prefix_lens;
   if (opt.softcap > 0.f) {
     prm.cap_log2 = opt.softcap * 1.4426950408889634f;
+    prm.cap_x = a.scale / opt.softcap;
     prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
   }
   const int64_t items = static_cast<int64_t>(prm.n_qt) * a.B * a.Hq;
