@@ -1,48 +1,829 @@
-// prefill_scored.cu — paged (chunked) prefill whose scores are capped or biased
-// by distance and whose rows see an interval of keys (pkv_score_options: a
-// window, documents, a two-way prefix), on the tensor-core kernel of
-// prefill_kernel.cuh.
+// prefill_scored.cu — paged (chunked) prefill attention whose scores are capped
+// or biased by distance and whose rows see an interval of keys
+// (pkv_score_options: a window, documents, a two-way prefix), on the sm_103a
+// tensor cores (tcgen05, tensor memory, TMA).
+//
+// Mathematics.  Row r of a chunk lies at position i = Lk - Lq + r and sees the
+// keys [lo, hi]; s = scale <q, K_j>, capped to c tanh(s / c), less slope |i - j|.
+// One pass over the key tiles with a running maximum and sum in log2 units:
+// O = sum 2^(s - m) V_j, l = sum 2^(s - m), out = O / l, lse = m + log2 l.
+//
+// Work item: 128 rows of one sequence and query head, and the 128-key tiles from
+// the lowest lo to the highest hi of those rows, so that a window or a document
+// costs its own tiles.  Persistent: one block per SM walks the items.  16 warps:
+//   warp 12 (TMA)  finds the next item, publishes it to the other warps through
+//                  a ring of descriptors, loads its K tiles and its Q.
+//   warp 13 (TMA)  V tiles.
+//   warp 14 (MMA)  S_t = Q K_t^T into one of three S buffers in tensor memory.
+//   warp 15 (MMA)  O += P_t V_t, A = P_t from tensor memory, B = V_t MN-major.
+//   warps 0-11     softmax, in three groups of four: group t % 3 takes tile t of
+//                  the block's running count, thread t of a group row t of the
+//                  tile (32 consecutive TMEM lanes a warp).
+// The softmax of a tile is a long chain (load S, maximum, 2^x, store P), some 8
+// to 14 instructions a pair of scores, and with every warp on every tile the
+// chain's latency is the time of a tile: two warps a scheduler on half a row
+// each ran at 45% of the issue rate (b16 below: 249 us), four on a quarter at
+// 50% (268 us).  Three tiles in flight overlap the chains.  What the groups hand
+// on from tile t to t + 1, row by row through shared memory: the running maximum
+// m(t), as soon as the tile's maximum is known and before its 2^x, and the
+// running sum l(t), after them.  m moves only when a tile exceeds it by 2^60, so
+// that O is hardly ever rescaled.  The group that takes the first tile of the next
+// item also writes the item's output, before its P is handed to the MMA.
+// TMEM (512 columns): S_0 | S_1 | S_2 | O; P overlays the first 64 columns of its
+// S, in 32-key chunks behind the chunk being read.
+// Every wait is bounded: a wait that runs out records an error, the block drains
+// what it started, frees its tensor memory and exits.
 
-#include "prefill_kernel.cuh"
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "pipeline.cuh"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
 
 namespace pkv {
+namespace {
+
+constexpr int kM = 128;   // query rows per tile
+constexpr int kN = 128;   // keys per tile
+constexpr int kGroups = 3;                 // softmax groups of four warps
+constexpr int kSoftmaxWarps = 4 * kGroups;
+constexpr int kQKWarp = kSoftmaxWarps;
+constexpr int kVWarp = kQKWarp + 1;
+constexpr int kSWarp = kQKWarp + 2;
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
+constexpr int kHalf = 128 * 128;           // 128 rows x 64 bf16 (one 128-byte swizzled box)
+constexpr int kTile = 2 * kHalf;           // 128 rows x 128 bf16
+constexpr int kKStages = 3;
+constexpr int kVStages = 3;
+constexpr int kSBufs = 3;
+static_assert(kGroups == kSBufs && kGroups == kVStages, "a group has an S buffer and V stage");
+constexpr int kRing = 4;                   // item descriptors
+constexpr int kOffQ = 0;                              // one buffer
+constexpr int kOffK = kOffQ + kTile;                  // kKStages stages
+constexpr int kOffV = kOffK + kKStages * kTile;       // kVStages stages
+constexpr int kOffM = kOffV + kVStages * kTile;       // m(t): [t & 1][row] fp32
+constexpr int kOffL = kOffM + 2 * kM * 4;             // l(t): [t & 1][row] fp32
+constexpr int kOffItems = kOffL + 2 * kM * 4;         // kRing descriptors
+constexpr int kItemBytes = 48;
+constexpr int kOffBars = kOffItems + kRing * kItemBytes;
+// barriers
+constexpr int kBarQFull = 0;
+constexpr int kBarQEmpty = 1;
+constexpr int kBarKFull = 2;                       // [K stage]
+constexpr int kBarKEmpty = kBarKFull + kKStages;
+constexpr int kBarVFull = kBarKEmpty + kKStages;   // [V stage]
+constexpr int kBarVEmpty = kBarVFull + kVStages;
+constexpr int kBarSFull = kBarVEmpty + kVStages;   // [S buffer]
+constexpr int kBarPFull = kBarSFull + kSBufs;      // [S buffer], its group's warps
+constexpr int kBarPVDone = kBarPFull + kSBufs;     // [S buffer]: the PV that read P has completed
+constexpr int kBarOFull = kBarPVDone + kSBufs;     // the last PV of an item has completed
+constexpr int kBarDrainS = kBarOFull + 1;
+constexpr int kBarDrainPV = kBarDrainS + 1;
+constexpr int kBarItemFull = kBarDrainPV + 1;      // [descriptor]
+constexpr int kBarItemEmpty = kBarItemFull + kRing;   // [descriptor], every other warp
+constexpr int kBarM = kBarItemEmpty + kRing;       // m(t) is there: [t & 1][row / 32]
+constexpr int kBarL = kBarM + 8;                   // l(t) is there: [t & 1][row / 32]
+constexpr int kNumBars = kBarL + 8;
+constexpr int kOffTmem = kOffBars + kNumBars * 8;
+constexpr int kOffFlags = kOffTmem + 8;
+constexpr int kSmemBytes = kOffFlags + 16;
+static_assert(kSmemBytes <= 227 * 1024, "one block per SM must fit in shared memory");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;      // + 128 * buffer
+constexpr uint32_t kColO = 384;
+// The running maximum moves when a tile's exceeds it by 2^60: weights up to 2^60
+// and their sums and products stay far inside fp32's range, at the same relative
+// precision, and moving it means waiting for the previous tile's PV.
+constexpr float kLazyRescale = 60.f;   // log2 units
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kTanhPoly = 0.625f;    // |s / softcap| up to which the cap is a polynomial
+
+struct Params {
+  __nv_bfloat16* out;
+  float* lse;
+  const int32_t* block_tables;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const float* slopes;         // per head, or null
+  const int32_t* first_keys;   // per row, or null
+  const int32_t* prefix_lens;  // per sequence, or null
+  unsigned* err;
+  int B, Hq, Hkv, maxblk, max_q, max_k, window;
+  int n_qt;          // ceil(max_q / 128)
+  int n_items;
+  int64_t num_blocks, total_q;
+  float scale_log2;  // raw product -> log2 units; capped: -> 2 log2(e) s / c
+  float cap_log2;    // the cap in log2 units
+  float cap_x;       // raw product -> s / c
+  float poly[5];     // c tanh(s / c) in log2 units = raw (poly[0] + poly[1] raw^2 + ...)
+};
+
+// One query tile and its keys.
+struct Item {
+  int n;          // key tiles (0: no more items)
+  int kt0;        // first key tile
+  int rows;       // valid query rows of the tile
+  int diag;       // position of the tile's first row
+  int kvh, h;     // kv head, query head
+  int row0;       // row of q / out of the tile's first row
+  int b;          // sequence
+  int prefix;     // tokens that every row sees
+  int vlo, vhi;   // keys outside [vlo, vhi] are hidden from every row and may hold
+                  // anything (vlo > vhi: no row has a key)
+};
+static_assert(sizeof(Item) <= kItemBytes, "descriptor");
+
+// Item idx, by a whole warp (the row bounds are reduced across it).
+__device__ __forceinline__ Item get_item(const Params& p, int idx, int lane) {
+  Item it = {};
+  const int per_lvl = p.B * p.Hq;
+  const int lvl = idx / per_lvl;             // heavier (later) row tiles first
+  const int rem = idx - lvl * per_lvl;
+  it.b = rem / p.Hq;
+  it.h = rem - it.b * p.Hq;
+  it.kvh = it.h / (p.Hq / p.Hkv);
+  const int q_begin = p.cu_q[it.b];
+  const int Lq = p.cu_q[it.b + 1] - q_begin;
+  const int Lk = p.cu_k[it.b + 1] - p.cu_k[it.b];
+  it.prefix = p.prefix_lens ? p.prefix_lens[it.b] : 0;
+  if (q_begin < 0 || Lq < 0 || q_begin + static_cast<int64_t>(Lq) > p.total_q || Lk < Lq ||
+      Lq > p.max_q || Lk > p.max_k ||
+      static_cast<int64_t>(Lk) > static_cast<int64_t>(p.maxblk) * kBlockSize || it.prefix < 0 ||
+      it.prefix > Lk) {
+    if (lane == 0) record_error(p.err, kErrIndex);
+    return it;
+  }
+  const int q0 = (p.n_qt - 1 - lvl) * kM;
+  if (q0 >= Lq) return it;
+  it.rows = min(kM, Lq - q0);
+  it.row0 = q_begin + q0;
+  it.diag = Lk - Lq + q0;
+  int klo = p.window > 0 ? max(0, it.diag - p.window + 1) : 0;
+  int khi = max(it.diag + it.rows - 1, it.prefix - 1);
+  it.vlo = p.window > 0 ? max(0, Lk - Lq - p.window + 1) : 0;
+  it.vhi = Lk - 1;
+  if (p.first_keys) {
+    klo = INT32_MAX;
+    khi = -1;
+    for (int r = lane; r < it.rows; r += 32) {
+      const int i = it.diag + r;
+      const int lo = max(p.window > 0 ? max(0, i - p.window + 1) : 0,
+                         __ldg(p.first_keys + it.row0 + r));
+      const int hi = max(i, it.prefix - 1);
+      if (lo <= hi) {
+        klo = min(klo, lo);
+        khi = max(khi, hi);
+      }
+    }
+    klo = __reduce_min_sync(kFull, klo);
+    khi = __reduce_max_sync(kFull, khi);
+    it.vlo = klo;
+    it.vhi = khi;
+    if (klo > khi) klo = khi = 0;   // no row has a key: one tile, all of it hidden
+  }
+  it.kt0 = klo / kN;
+  it.n = khi / kN - it.kt0 + 1;
+  return it;
+}
+
+// Item of round k for this block: rounds alternate direction so that every
+// block gets a mix of heavy and light items.
+__device__ __forceinline__ int item_index(int k) {
+  const int c = (k & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)
+                        : static_cast<int>(blockIdx.x);
+  return k * static_cast<int>(gridDim.x) + c;
+}
+
+template <bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const Params p) {
+  // (no room for a realignment: the tiles' 128-byte swizzle wants 1024 bytes)
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_addr(smem);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) record_error(p.err, kErrTimeout);
+    return;
+  }
+  const uint32_t bars = sbase + kOffBars;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  volatile int* flags = reinterpret_cast<volatile int*>(smem + kOffFlags);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kOffTmem);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t count = 1;
+      if (i >= kBarPFull && i < kBarPFull + kSBufs) count = 4;
+      if (i >= kBarItemEmpty && i < kBarItemEmpty + kRing) count = kSoftmaxWarps + 3;
+      mbar_init(bar(i), count);
+    }
+    flags[0] = 0;  // abort
+    flags[1] = 0;  // K tiles issued
+    flags[2] = 0;  // V tiles issued
+    flags[3] = 0;  // Q tiles issued
+    fence_barrier_init();
+  }
+  if (warp == kSWarp) {
+    tmem_alloc(sbase + kOffTmem, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == kQKWarp && lane == 0) {
+    tma_prefetch_map(&qmap);
+    tma_prefetch_map(&kmap);
+  }
+  if (warp == kVWarp && lane == 0) tma_prefetch_map(&vmap);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The block's gi-th item, for every warp but the one that publishes them;
+  // false: a wait ran out.
+  auto take_item = [&](int gi, Item& it) -> bool {
+    const int slot = gi % kRing;
+    if (!warp_wait(bar(kBarItemFull + slot), (gi / kRing) & 1)) return false;
+    it = *reinterpret_cast<const Item*>(smem + kOffItems + slot * kItemBytes);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
+    return true;
+  };
+
+  if (warp >= kSoftmaxWarps) {
+    bool ok = true, timeout = false;
+    if (warp == kQKWarp) {
+      // ---------------------------------------------------------- items, K and Q
+      // An item's Q goes into the single Q buffer right after its first K tile
+      // has been issued, once the S MMAs of the previous item are done with it.
+      const int n_rounds = (p.n_items + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+      int gk = 0, round = 0;
+      BlockIds ids;
+      Ring<kKStages> rk;
+      const int withhold = withheld_tile();   // test hook: K tiles from here on are never copied
+      for (int gi = 0; ok; ++gi) {
+        Item it = {};
+        for (; round < n_rounds && it.n == 0; ++round) {
+          const int idx = item_index(round);
+          if (idx < p.n_items) it = get_item(p, idx, lane);
+        }
+        const int slot = gi % kRing;
+        if (gi >= kRing && !warp_wait(bar(kBarItemEmpty + slot), (gi / kRing - 1) & 1)) {
+          ok = false;
+          timeout = true;
+          break;
+        }
+        if (lane == 0) {
+          *reinterpret_cast<Item*>(smem + kOffItems + slot * kItemBytes) = it;
+          mbar_arrive(bar(kBarItemFull + slot));
+        }
+        __syncwarp();
+        if (it.n == 0) break;
+        const int32_t* table = p.block_tables + static_cast<int64_t>(it.b) * p.maxblk;
+        ids.chunk = -1;
+        bool stopped = false;
+        for (int kt = 0; kt < it.n; ++kt, ++gk, rk.next()) {
+          if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
+          if (gk >= withhold) { stopped = true; break; }
+          const int gkt = it.kt0 + kt;
+          // (an item without keys reads no table entry)
+          const int id = it.vlo > it.vhi
+                             ? 0 : ids.get(table, p.maxblk, gkt >> 1, lane, p.num_blocks, p.err);
+          const int at = id * kBlockSize + (gkt & 1) * kN;
+          if (gk >= kKStages && !warp_wait(bar(kBarKEmpty + rk.idx), rk.ph ^ 1u)) {
+            ok = false;
+            timeout = true;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kBarKFull + rk.idx), kTile);
+            flags[1] = gk + 1;
+          }
+          __syncwarp();
+          // lanes 2s, 2s+1 load stage s: a lane's next copy never queues behind
+          // its previous one
+          if ((lane >> 1) == rk.idx)
+            tma_load_3d(sbase + kOffK + rk.idx * kTile + (lane & 1) * kHalf, &kmap,
+                        bar(kBarKFull + rk.idx), (lane & 1) * 64, it.kvh, at);
+          __syncwarp();
+          if (kt == 0) {
+            if (gi >= 1 && !warp_wait(bar(kBarQEmpty), (gi - 1) & 1)) {
+              ok = false;
+              timeout = true;
+              break;
+            }
+            if (lane == 0) {
+              // rows past the sequence are its neighbour's, or zeros past total_q
+              mbar_arrive_expect_tx(bar(kBarQFull), kTile);
+              flags[3] = gi + 1;
+            }
+            __syncwarp();
+            if (lane >= 2 * kKStages && lane < 2 * kKStages + 2)   // lanes of their own
+              tma_load_3d(sbase + kOffQ + (lane & 1) * kHalf, &qmap, bar(kBarQFull),
+                          (lane & 1) * 64, it.h, it.row0);
+            __syncwarp();
+          }
+        }
+        if (stopped) break;
+      }
+    } else if (warp == kVWarp) {
+      // ---------------------------------------------------------- V
+      int gk = 0;
+      BlockIds ids;
+      Ring<kVStages> rv;
+      for (int gi = 0; ok; ++gi) {
+        Item it;
+        if (!take_item(gi, it)) { ok = false; timeout = true; break; }
+        if (it.n == 0) break;
+        const int32_t* table = p.block_tables + static_cast<int64_t>(it.b) * p.maxblk;
+        ids.chunk = -1;
+        for (int kt = 0; kt < it.n; ++kt, ++gk, rv.next()) {
+          if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
+          const int gkt = it.kt0 + kt;
+          const int id = it.vlo > it.vhi
+                             ? 0 : ids.get(table, p.maxblk, gkt >> 1, lane, p.num_blocks, p.err);
+          const int at = id * kBlockSize + (gkt & 1) * kN;
+          if (gk >= kVStages && !warp_wait(bar(kBarVEmpty + rv.idx), rv.ph ^ 1u)) {
+            ok = false;
+            timeout = true;
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kBarVFull + rv.idx), kTile);
+            flags[2] = gk + 1;
+          }
+          __syncwarp();
+          if ((lane >> 1) == rv.idx)
+            tma_load_3d(sbase + kOffV + rv.idx * kTile + (lane & 1) * kHalf, &vmap,
+                        bar(kBarVFull + rv.idx), (lane & 1) * 64, it.kvh, at);
+          __syncwarp();
+        }
+      }
+    } else if (warp == kSWarp) {
+      // ---------------------------------------------------------- MMA: S = Q K^T
+      // (the whole warp runs the loop and waits; an elected lane issues)
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kM, kN, 0);   // B = K, K-major
+      int gk = 0;
+      Ring<kSBufs> sb;
+      Ring<kKStages> rk;
+      for (int gi = 0; ok; ++gi) {
+        Item it;
+        if (!take_item(gi, it)) { ok = false; timeout = true; break; }
+        if (it.n == 0) break;
+        if (!warp_wait(bar(kBarQFull), gi & 1)) { ok = false; timeout = true; break; }
+        const uint32_t q_s = sbase + kOffQ;
+        for (int kt = 0; kt < it.n; ++kt, ++gk, sb.next(), rk.next()) {
+          if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
+          // K here, and the S buffer free: the PV that read P from it (three
+          // tiles back) is done
+          if (!warp_wait(bar(kBarKFull + rk.idx), rk.ph) ||
+              (gk >= kSBufs && !warp_wait(bar(kBarPVDone + sb.idx), sb.ph ^ 1u))) {
+            ok = false;
+            timeout = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t k_s = sbase + kOffK + rk.idx * kTile;
+          const uint32_t d_s = tmem + kColS + sb.idx * kN;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 32;
+            umma_bf16_warp(d_s, smem_desc_sw128(q_s + off, 16, 1024),
+                           smem_desc_sw128(k_s + off, 16, 1024), idesc_s, ks > 0);
+          }
+          umma_commit_warp(bar(kBarSFull + sb.idx));
+          umma_commit_warp(bar(kBarKEmpty + rk.idx));
+        }
+        if (!ok) break;
+        umma_commit_warp(bar(kBarQEmpty));
+      }
+      // every MMA this warp issued has completed once this arrives
+      umma_commit_warp(bar(kBarDrainS));
+      (void)warp_wait(bar(kBarDrainS), 0);
+    } else {
+      // ---------------------------------------------------------- MMA: O += P V
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kM, kHeadDim, 1);  // B = V, MN-major
+      Ring<kSBufs> sb;
+      Ring<kVStages> rv;
+      const uint32_t d_o = tmem + kColO;
+      for (int gi = 0; ok; ++gi) {
+        Item it;
+        if (!take_item(gi, it)) { ok = false; timeout = true; break; }
+        if (it.n == 0) break;
+        for (int kt = 0; kt < it.n; ++kt, sb.next(), rv.next()) {
+          if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
+          if (!warp_wait(bar(kBarVFull + rv.idx), rv.ph) ||
+              !warp_wait(bar(kBarPFull + sb.idx), sb.ph)) {
+            ok = false;
+            timeout = true;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t v_s = sbase + kOffV + rv.idx * kTile;
+          const uint32_t p_t = tmem + kColS + sb.idx * kN;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            // A = P: 16 keys = 8 packed columns per step.  B = V: 64-dim boxes
+            // kHalf apart (LBO), 8-key swizzle atoms 1024 bytes apart (SBO).
+            umma_bf16_tmem_a_warp(d_o, p_t + ks * 8, smem_desc_sw128(v_s + ks * 2048, kHalf, 1024),
+                                  idesc_o, (kt > 0 || ks > 0) ? 1u : 0u);
+          }
+          umma_commit_warp(bar(kBarVEmpty + rv.idx));
+          umma_commit_warp(bar(kBarPVDone + sb.idx));
+        }
+        if (!ok) break;
+        umma_commit_warp(bar(kBarOFull));
+      }
+      umma_commit_warp(bar(kBarDrainPV));
+      (void)warp_wait(bar(kBarDrainPV), 0);
+    }
+    if (timeout && lane == 0) record_error(p.err, kErrTimeout);
+    if (!ok && lane == 0) flags[0] = 1;
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int group = warp >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;   // this thread's row of every tile
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_col = lane_base + kColS + group * kN;
+    const uint32_t o_col = lane_base + kColO;
+    float* const m_slot = reinterpret_cast<float*>(smem + kOffM) + row;
+    float* const l_slot = reinterpret_cast<float*>(smem + kOffL) + row;
+    bool ok = true, timeout = false;
+    const f32x2 sc2 = pack2(p.scale_log2, p.scale_log2);
+
+    // m(t) and l(t) pass through two slots each: the writer of t + 2 has read the
+    // value of t + 1, whose writer had read that of t.
+    auto hand_on = [&](int first_bar, float* slot, int t, float v) {
+      slot[(t & 1) * kM] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(first_bar + (t & 1) * 4 + quarter));
+    };
+    auto receive = [&](int first_bar, const float* slot, int t, float& v) -> bool {
+      if (!warp_wait(bar(first_bar + (t & 1) * 4 + quarter), (t >> 1) & 1)) return false;
+      v = *const_cast<const volatile float*>(slot + (t & 1) * kM);
+      return true;
+    };
+    // Output of finished item number `done` (its m and l): O / l, row by row.
+    auto epilogue = [&](const Item& e, int done, float m, float l) -> bool {
+      if (!warp_wait(bar(kBarOFull), done & 1)) return false;
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;   // a row without keys: 0 and -inf
+      const bool valid = row < e.rows;
+      const int64_t at = static_cast<int64_t>(e.row0 + row) * p.Hq + e.h;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32x32_x32(o_col + 32 * c, o);
+        tmem_wait_ld(o);
+        if (valid) {
+          auto two = [&](int k) {
+            return pack_bf16x2(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
+          };
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[4 * c + k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+        }
+      }
+      if (p.lse && valid) p.lse[at] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      return true;
+    };
+
+    Item prev = {};
+    int gi = 0, t_item = 0;   // items, and the running count of the item's first tile
+    for (; ok; ++gi) {
+      Item it;
+      if (!take_item(gi, it)) { ok = false; timeout = true; break; }
+      if (it.n == 0) break;
+      // position of the row, the keys [lo, hi] it sees, the head's slope in log2 units
+      const int pos = it.diag + row;
+      int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+      if (p.first_keys && row < it.rows) lo = max(lo, __ldg(p.first_keys + it.row0 + row));
+      const int hi = max(pos, it.prefix - 1);
+      float slope = 0.f;
+      if constexpr (kBias) slope = __ldg(p.slopes + it.h) * 1.4426950408889634f;
+      const f32x2 slope2 = pack2(slope, slope);
+
+      int kt = group - t_item % kGroups;
+      if (kt < 0) kt += kGroups;
+      for (; kt < it.n; kt += kGroups) {
+        const int t = t_item + kt;
+        const uint32_t ph = (t / kGroups) & 1;   // of the group's S buffer and V stage
+        if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
+        if (!(ok = warp_wait(bar(kBarSFull + group), ph))) { timeout = true; break; }
+        tc_fence_after();
+        const int tile = (it.kt0 + kt) * kN;
+        // the row's keys within the tile: c with c - c_lo <= span, unsigned
+        const int c_lo = lo > hi ? 1 << 30 : lo - tile;
+        const unsigned span = lo > hi ? 0u : static_cast<unsigned>(hi - lo);
+        const bool edge = __any_sync(kFull, c_lo > 0 || c_lo + static_cast<int64_t>(span) < kN - 1);
+        auto hidden = [&](int c) { return static_cast<unsigned>(c - c_lo) > span; };
+        // Biased: -slope |pos - j| = slope c + slope (tile - pos) for key j = tile + c
+        // up to the row's own position; the second part is a constant of row and
+        // tile, off.  Past that position (a two-way prefix) it is 2 slope (c - past)
+        // less, past = pos - tile.
+        const float past = static_cast<float>(pos - tile);
+        const float off = kBias ? -slope * past : 0.f;
+        const bool two_way = kBias && it.prefix > 0;
+        auto bias = [&](auto both, f32x2 c, f32x2 add) {
+          f32x2 b = fma2(c, slope2, add);
+          if constexpr (both)
+            b = fma2(pack2(fmaxf(lo2(c) - past, 0.f), fmaxf(hi2(c) - past, 0.f)),
+                     pack2(-2.f * slope, -2.f * slope), b);
+          return b;
+        };
+        // Capped: c tanh(s / c), s / c = x.  While |x| <= 0.625 in the whole warp: an
+        // odd polynomial (minimax for the absolute error, 3e-8, computed by exchange
+        // for this interval), on the FMA pipe.  Else c - 2c / (1 + e^2x), with two
+        // special-function operations, which are scarcer.
+        auto near_cap = [&](f32x2 v, f32x2 add) {
+          const f32x2 u = mul2(v, v);
+          f32x2 y = fma2(pack2(p.poly[4], p.poly[4]), u, pack2(p.poly[3], p.poly[3]));
+          y = fma2(y, u, pack2(p.poly[2], p.poly[2]));
+          y = fma2(y, u, pack2(p.poly[1], p.poly[1]));
+          y = fma2(y, u, pack2(p.poly[0], p.poly[0]));
+          return fma2(v, y, add);
+        };
+        auto far_cap = [&](f32x2 v, f32x2 add) {
+          v = mul2(v, sc2);
+          v = add2(pack2(ex2(lo2(v)), ex2(hi2(v))), pack2(1.f, 1.f));
+          return add2(fma2(pack2(rcp_approx(lo2(v)), rcp_approx(hi2(v))),
+                           pack2(-2.f * p.cap_log2, -2.f * p.cap_log2),
+                           pack2(p.cap_log2, p.cap_log2)), add);
+        };
+        auto plain = [&](f32x2 v, f32x2 add) { return fma2(v, sc2, add); };
+
+        // First pass: the row's maximum.  Unbiased: of the products, as the cap is
+        // increasing.  Biased: of the scores less `off`.
+        float mx = -INFINITY;
+        bool far = false;
+        uint32_t r0[32];
+        auto chunk_max = [&](const uint32_t (&r)[32], int c0) {
+          if (edge) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!hidden(c0 + c)) mx = fmaxf(mx, __uint_as_float(r[c]));
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2)
+              mx = max3(mx, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+          }
+        };
+        if constexpr (kCap || !kBias) {
+          float big = 0.f;
+          auto chunk_big = [&](const uint32_t (&r)[32]) {
+#pragma unroll
+            for (int c = 0; c < 32; c += 2)
+              big = absmax3(big, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
+          };
+#pragma unroll 1
+          for (int c0 = 0; c0 < kN; c0 += 32) {
+            tmem_ld32x32_x32(s_col + c0, r0);
+            tmem_wait_ld(r0);
+            if constexpr (kCap) chunk_big(r0);
+            if constexpr (!kBias) chunk_max(r0, c0);
+          }
+          if constexpr (kCap) far = __any_sync(kFull, !(big * p.cap_x <= kTanhPoly));
+        }
+        if constexpr (kBias) {
+          auto scan = [&](auto both, auto score) {
+            f32x2 c2 = pack2(0.f, 1.f);
+#pragma unroll 1
+            for (int c0 = 0; c0 < kN; c0 += 32) {
+              tmem_ld32x32_x32(s_col + c0, r0);
+              tmem_wait_ld(r0);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const f32x2 v = score(pack2(__uint_as_float(r0[c]), __uint_as_float(r0[c + 1])),
+                                      bias(both, c2, pack2(0.f, 0.f)));
+                c2 = add2(c2, pack2(2.f, 2.f));
+                r0[c] = __float_as_uint(lo2(v));
+                r0[c + 1] = __float_as_uint(hi2(v));
+              }
+              chunk_max(r0, c0);
+            }
+          };
+          auto scan_with = [&](auto both) {
+            if (!kCap)
+              scan(both, plain);
+            else if (far)
+              scan(both, far_cap);
+            else
+              scan(both, near_cap);
+          };
+          if (two_way)
+            scan_with(std::true_type{});
+          else
+            scan_with(std::false_type{});
+          mx += off;
+        } else if constexpr (kCap) {
+          if (mx > -INFINITY)
+            mx = fmaf(-2.f * p.cap_log2, rcp_approx(1.f + ex2(mx * p.scale_log2)), p.cap_log2);
+        } else {
+          mx *= p.scale_log2;
+        }
+
+        // The running maximum.  (Received for an item's first tile as well: its
+        // slot is then free, and it is the m of the item to write.)
+        float m_before = -INFINITY;
+        if (t > 0 && !(ok = receive(kBarM, m_slot, t - 1, m_before))) { timeout = true; break; }
+        const bool need = kt > 0 && mx > m_before + kLazyRescale;
+        const float m = kt > 0 && !need ? m_before : mx;
+        float alpha = 1.f;
+        hand_on(kBarM, m_slot, t, m);   // before the rescaling, which waits
+        if (need) alpha = ex2(m_before - mx);
+        if (kt > 0) {
+          // (a row without keys so far has O = 0 at any m)
+          if (__any_sync(kFull, need && m_before > -INFINITY)) {
+            // the previous tile's PV must have finished accumulating into O
+            if (!(ok = warp_wait(bar(kBarPVDone + (t - 1) % kSBufs), ((t - 1) / kSBufs) & 1))) {
+              timeout = true;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32x32_x32(o_col + 32 * c, r0);
+              tmem_wait_ld(r0);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) r0[k] = __float_as_uint(__uint_as_float(r0[k]) * alpha);
+              tmem_st32x32_x32(o_col + 32 * c, r0);
+            }
+          }
+        }
+
+        // Second pass: P = 2^(s - m) as bf16 pairs, column c / 2 for keys c, c + 1.  A
+        // hidden key gets weight 0; a row that has seen no key yet has m = -inf and
+        // hidden keys only.
+        const float base = m == -INFINITY ? 0.f : off - m;
+        const f32x2 base2 = pack2(base, base);
+        f32x2 sum2 = pack2(0.f, 0.f);
+        auto weigh = [&](auto is_edge, auto both, auto score) {
+          f32x2 c2 = pack2(0.f, 1.f);
+          auto chunk = [&](const uint32_t (&r)[32], int c0) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              f32x2 add = base2;
+              if constexpr (kBias) {
+                add = bias(both, c2, base2);
+                c2 = add2(c2, pack2(2.f, 2.f));
+              }
+              const f32x2 x = score(pack2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), add);
+              float w0 = ex2(lo2(x)), w1 = ex2(hi2(x));
+              if constexpr (is_edge) {
+                if (hidden(c0 + c)) w0 = 0.f;
+                if (hidden(c0 + c + 1)) w1 = 0.f;
+              }
+              pk[c / 2] = pack_bf16x2(w0, w1);
+              sum2 = add2(sum2, pack2(w0, w1));
+            }
+            tmem_st32x32_x16(s_col + c0 / 2, pk);
+          };
+#pragma unroll 1
+          for (int c0 = 0; c0 < kN; c0 += 32) {
+            tmem_ld32x32_x32(s_col + c0, r0);
+            tmem_wait_ld(r0);
+            chunk(r0, c0);
+          }
+        };
+        auto weigh_with = [&](auto is_edge, auto both) {
+          if constexpr (!kCap) {
+            weigh(is_edge, both, plain);
+          } else if (far) {
+            weigh(is_edge, both, far_cap);
+          } else {
+            weigh(is_edge, both, near_cap);
+          }
+        };
+        if (two_way)
+          weigh_with(std::true_type{}, std::integral_constant<bool, kBias>{});
+        else if (edge)
+          weigh_with(std::true_type{}, std::false_type{});
+        else
+          weigh_with(std::false_type{}, std::false_type{});
+
+        // keys outside [vlo, vhi]: zero their V rows so that 0 * (stale data)
+        // cannot put a NaN into O (the group's thread s clears row s)
+        if ((kt == 0 && tile < it.vlo) || (kt == it.n - 1 && tile + kN - 1 > it.vhi)) {
+          if (!(ok = warp_wait(bar(kBarVFull + group), ph))) { timeout = true; break; }
+          if (tile + row < it.vlo || tile + row > it.vhi) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const uint32_t vrow = sbase + kOffV + group * kTile + row * 128;
+#pragma unroll
+            for (int cc = 0; cc < 8; ++cc) {
+              sts128(vrow + cc * 16, zero);
+              sts128(vrow + kHalf + cc * 16, zero);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        float l = lo2(sum2) + hi2(sum2), l_before = 0.f;
+        if (kt == 0 && t > 0) {   // this tile's PV will overwrite O: write the last item first
+          if (!(ok = receive(kBarL, l_slot, t - 1, l_before) &&
+                     epilogue(prev, gi - 1, m_before, l_before))) {
+            timeout = true;
+            break;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarPFull + group));
+        if (kt > 0) {
+          if (!(ok = receive(kBarL, l_slot, t - 1, l_before))) { timeout = true; break; }
+          l = fmaf(l_before, alpha, l);
+        }
+        hand_on(kBarL, l_slot, t, l);
+      }
+      if (!ok) break;
+      prev = it;
+      t_item += it.n;
+    }
+    if (ok && t_item > 0 && t_item % kGroups == group) {   // the last item's output
+      float m, l;
+      if (!(ok = receive(kBarM, m_slot, t_item - 1, m) && receive(kBarL, l_slot, t_item - 1, l) &&
+                 epilogue(prev, gi - 1, m, l)))
+        timeout = true;
+    }
+    if (timeout && lane == 0) record_error(p.err, kErrTimeout);
+    if (!ok && lane == 0) flags[0] = 1;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // After an abort, wait (bounded) for TMA copies that may still be landing:
+  // the last issued tiles of each ring.
+  if (flags[0] && tid == kQKWarp * 32) {
+    const int kin = flags[1], qin = flags[3];
+    for (int x = max(0, kin - kKStages); x < kin; ++x)
+      (void)mbar_wait(bar(kBarKFull + x % kKStages), (x / kKStages) & 1);
+    if (qin > 0) (void)mbar_wait(bar(kBarQFull), (qin - 1) & 1);
+  }
+  if (flags[0] && tid == kVWarp * 32) {
+    const int vin = flags[2];
+    for (int x = max(0, vin - kVStages); x < vin; ++x)
+      (void)mbar_wait(bar(kBarVFull + x % kVStages), (x / kVStages) & 1);
+  }
+  __syncthreads();
+  if (warp == kSWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <bool kCap, bool kBias>
+int launch_form(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
+                const Params& prm, cudaStream_t stream) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    if (cudaFuncSetAttribute(scored_prefill_kernel<kCap, kBias>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemBytes) != cudaSuccess)
+      return PKV_ERR_LAUNCH;
+    attr_set[dev] = true;
+  }
+  int sms = device_sm_count();
+  if (sms <= 0) sms = 148;
+  const int grid = prm.n_items < sms ? prm.n_items : sms;
+  scored_prefill_kernel<kCap, kBias><<<grid, kThreads, kSmemBytes, stream>>>(qm, km, vm, prm);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
+}
+
+}  // namespace
 
 int set_wait_hook_prefill_scored(unsigned long long limit_ns, int withhold_plus1) {
   const WaitHook h{limit_ns, withhold_plus1, 0};
   return cudaMemcpyToSymbol(g_wait_hook, &h, sizeof h) == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
-namespace {
-
-template <bool kCap, bool kBias>
-int launch_form(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                const PrefillParams& prm, cudaStream_t stream) {
-  if (!set_smem_attr<kScored, kCap, kBias>()) return PKV_ERR_LAUNCH;
-  paged_prefill_kernel<kScored, kCap, kBias>
-      <<<grid_for(prm.n_items), kThreads, kSmemBytes, stream>>>(qm, km, vm, prm);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
-}
-
-}  // namespace
-
 int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score_options& opt,
                           unsigned* err, cudaStream_t stream) {
   if (a.B == 0 || a.max_seqlen_q == 0 || total_q == 0) return PKV_OK;
   CUtensorMap qm, km, vm;
   const int64_t slots = a.num_blocks * kBlockSize;
-  // q holds exactly total_q rows: a ragged tile reads its neighbour's rows, or
-  // zeros past the end, and stores none of them
   if (!encode_pool_map(&qm, a.q, total_q, a.Hq, kM) ||
       !encode_pool_map(&km, a.k_cache, slots, a.Hkv, kN) ||
       !encode_pool_map(&vm, a.v_cache, slots, a.Hkv, kN))
     return PKV_ERR_ARG;
-  PrefillParams prm = {};
+  Params prm = {};
   prm.out = static_cast<__nv_bfloat16*>(a.out);
   prm.lse = a.lse;
-  prm.q = static_cast<const __nv_bfloat16*>(a.q);
   prm.block_tables = a.block_tables;
   prm.cu_q = a.cu_seqlens_q;
   prm.cu_k = a.cu_seqlens_k;
+  prm.slopes = opt.alibi_slopes;
+  prm.first_keys = opt.first_keys;
+  prm.prefix_lens = opt.prefix_lens;
   prm.err = err;
   prm.B = a.B;
   prm.Hq = a.Hq;
@@ -50,28 +831,32 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   prm.maxblk = a.max_blocks_per_seq;
   prm.max_q = a.max_seqlen_q;
   prm.max_k = a.max_seqlen_k;
-  prm.n_qt = (a.max_seqlen_q + kM - 1) / kM;
-  prm.num_blocks = a.num_blocks;
-  prm.scale_log2 = a.scale * 1.4426950408889634f;
-  prm.total_q = total_q;
   prm.window = opt.window;
-  prm.slopes = opt.alibi_slopes;
-  prm.first_keys = opt.first_keys;
-  prm.prefix_lens = opt.prefix_lens;
-  if (opt.softcap > 0.f) {
-    prm.cap_log2 = opt.softcap * 1.4426950408889634f;
-    prm.cap_x = a.scale / opt.softcap;
-    prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
-  }
+  prm.n_qt = (a.max_seqlen_q + kM - 1) / kM;
   const int64_t items = static_cast<int64_t>(prm.n_qt) * a.B * a.Hq;
   if (items > INT32_MAX) return PKV_ERR_SHAPE;
   prm.n_items = static_cast<int>(items);
+  prm.num_blocks = a.num_blocks;
+  prm.total_q = total_q;
   const bool cap = opt.softcap > 0.f, bias = opt.alibi_slopes != nullptr;
-  if (cap)
-    return bias ? launch_form<true, true>(qm, km, vm, prm, stream)
-                : launch_form<true, false>(qm, km, vm, prm, stream);
-  return bias ? launch_form<false, true>(qm, km, vm, prm, stream)
-              : launch_form<false, false>(qm, km, vm, prm, stream);
+  if (!cap) {
+    prm.scale_log2 = a.scale * 1.4426950408889634f;
+    return bias ? launch_form<false, true>(qm, km, vm, prm, stream)
+                : launch_form<false, false>(qm, km, vm, prm, stream);
+  }
+  prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
+  prm.cap_log2 = opt.softcap * 1.4426950408889634f;
+  prm.cap_x = a.scale / opt.softcap;
+  // tanh(x) = x (t0 + t1 x^2 + ...) on |x| <= 0.625, x = raw * cap_x; the powers
+  // of cap_x are folded into the coefficients, unless they would leave fp32's
+  // range: every product then takes the exact form
+  const double t[5] = {0.999999459, -0.333304827, 0.132910316, -0.0513628685, 0.0145300686};
+  double f = static_cast<double>(prm.cap_log2) * prm.cap_x;
+  for (int k = 0; k < 5; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
+    prm.poly[k] = static_cast<float>(t[k] * f);
+  if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) prm.cap_x = INFINITY;
+  return bias ? launch_form<true, true>(qm, km, vm, prm, stream)
+              : launch_form<true, false>(qm, km, vm, prm, stream);
 }
 
 }  // namespace pkv
