@@ -99,6 +99,9 @@ constexpr uint32_t kColO = 384;
 // precision, and moving it means waiting for the previous tile's PV.
 constexpr float kLazyRescale = 60.f;   // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
+// Caps up to this (log2 units) need no maximum: with m = 0 every weight lies in
+// 2^+-100, and sums of weights times values stay inside fp32's range.
+constexpr float kFixedCap = 100.f;
 constexpr float kTanhPoly = 0.625f;    // |s / softcap| up to which the cap is a polynomial
 
 struct Params {
@@ -197,7 +200,9 @@ __device__ __forceinline__ int item_index(int k) {
   return k * static_cast<int>(gridDim.x) + c;
 }
 
-template <bool kCap, bool kBias>
+// kCap: capped scores; kBias: biased ones; kFixed: capped by at most kFixedCap and
+// not biased, so that m = 0 throughout and one pass over a tile's scores is enough.
+template <bool kCap, bool kBias, bool kFixed>
 __global__ void __launch_bounds__(kThreads, 1)
 scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
@@ -549,22 +554,24 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           y = fma2(y, u, pack2(p.poly[2], p.poly[2]));
           y = fma2(y, u, pack2(p.poly[1], p.poly[1]));
           y = fma2(y, u, pack2(p.poly[0], p.poly[0]));
-          return fma2(v, y, add);
+          return kFixed ? mul2(v, y) : fma2(v, y, add);
         };
         auto far_cap = [&](f32x2 v, f32x2 add) {
           v = mul2(v, sc2);
           v = add2(pack2(ex2(lo2(v)), ex2(hi2(v))), pack2(1.f, 1.f));
-          return add2(fma2(pack2(rcp_approx(lo2(v)), rcp_approx(hi2(v))),
-                           pack2(-2.f * p.cap_log2, -2.f * p.cap_log2),
-                           pack2(p.cap_log2, p.cap_log2)), add);
+          v = fma2(pack2(rcp_approx(lo2(v)), rcp_approx(hi2(v))),
+                   pack2(-2.f * p.cap_log2, -2.f * p.cap_log2), pack2(p.cap_log2, p.cap_log2));
+          return kFixed ? v : add2(v, add);
         };
         auto plain = [&](f32x2 v, f32x2 add) { return fma2(v, sc2, add); };
 
+        uint32_t r0[32];
+        float m = 0.f, alpha = 1.f, m_before = 0.f;
+        bool far = false;
+        if constexpr (!kFixed) {
         // First pass: the row's maximum.  Unbiased: of the products, as the cap is
         // increasing.  Biased: of the scores less `off`.
         float mx = -INFINITY;
-        bool far = false;
-        uint32_t r0[32];
         auto chunk_max = [&](const uint32_t (&r)[32], int c0) {
           if (edge) {
 #pragma unroll
@@ -632,11 +639,9 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
 
         // The running maximum.  (Received for an item's first tile as well: its
         // slot is then free, and it is the m of the item to write.)
-        float m_before = -INFINITY;
         if (t > 0 && !(ok = receive(kBarM, m_slot, t - 1, m_before))) { timeout = true; break; }
         const bool need = kt > 0 && mx > m_before + kLazyRescale;
-        const float m = kt > 0 && !need ? m_before : mx;
-        float alpha = 1.f;
+        m = kt > 0 && !need ? m_before : mx;
         hand_on(kBarM, m_slot, t, m);   // before the rescaling, which waits
         if (need) alpha = ex2(m_before - mx);
         if (kt > 0) {
@@ -658,6 +663,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
             }
           }
         }
+        }   // !kFixed
 
         // Second pass: P = 2^(s - m) as bf16 pairs, column c / 2 for keys c, c + 1.  A
         // hidden key gets weight 0; a row that has seen no key yet has m = -inf and
@@ -665,37 +671,56 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         const float base = m == -INFINITY ? 0.f : off - m;
         const f32x2 base2 = pack2(base, base);
         f32x2 sum2 = pack2(0.f, 0.f);
-        auto weigh = [&](auto is_edge, auto both, auto score) {
-          f32x2 c2 = pack2(0.f, 1.f);
-          auto chunk = [&](const uint32_t (&r)[32], int c0) {
-            uint32_t pk[16];
+        f32x2 c2 = pack2(0.f, 1.f);   // (biased) the pair's keys within the tile
+        auto chunk = [&](auto is_edge, auto both, auto score, int c0) {
+          uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              f32x2 add = base2;
-              if constexpr (kBias) {
-                add = bias(both, c2, base2);
-                c2 = add2(c2, pack2(2.f, 2.f));
-              }
-              const f32x2 x = score(pack2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), add);
-              float w0 = ex2(lo2(x)), w1 = ex2(hi2(x));
-              if constexpr (is_edge) {
-                if (hidden(c0 + c)) w0 = 0.f;
-                if (hidden(c0 + c + 1)) w1 = 0.f;
-              }
-              pk[c / 2] = pack_bf16x2(w0, w1);
-              sum2 = add2(sum2, pack2(w0, w1));
+          for (int c = 0; c < 32; c += 2) {
+            f32x2 add = base2;
+            if constexpr (kBias) {
+              add = bias(both, c2, base2);
+              c2 = add2(c2, pack2(2.f, 2.f));
             }
-            tmem_st32x32_x16(s_col + c0 / 2, pk);
-          };
+            const f32x2 x = score(pack2(__uint_as_float(r0[c]), __uint_as_float(r0[c + 1])), add);
+            float w0 = ex2(lo2(x)), w1 = ex2(hi2(x));
+            if constexpr (is_edge) {
+              if (hidden(c0 + c)) w0 = 0.f;
+              if (hidden(c0 + c + 1)) w1 = 0.f;
+            }
+            pk[c / 2] = pack_bf16x2(w0, w1);
+            sum2 = add2(sum2, pack2(w0, w1));
+          }
+          tmem_st32x32_x16(s_col + c0 / 2, pk);
+        };
+        auto weigh = [&](auto is_edge, auto both, auto score) {
 #pragma unroll 1
           for (int c0 = 0; c0 < kN; c0 += 32) {
             tmem_ld32x32_x32(s_col + c0, r0);
             tmem_wait_ld(r0);
-            chunk(r0, c0);
+            chunk(is_edge, both, score, c0);
+          }
+        };
+        auto weigh_fixed = [&](auto is_edge) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < kN; c0 += 32) {
+            tmem_ld32x32_x32(s_col + c0, r0);
+            tmem_wait_ld(r0);
+            float big = 0.f, big2 = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+              big = absmax3(big, __uint_as_float(r0[c]), __uint_as_float(r0[c + 1]));
+              big2 = absmax3(big2, __uint_as_float(r0[c + 2]), __uint_as_float(r0[c + 3]));
+            }
+            if (__any_sync(kFull, !(fmaxf(big, big2) * p.cap_x <= kTanhPoly)))
+              chunk(is_edge, std::false_type{}, far_cap, c0);
+            else
+              chunk(is_edge, std::false_type{}, near_cap, c0);
           }
         };
         auto weigh_with = [&](auto is_edge, auto both) {
-          if constexpr (!kCap) {
+          if constexpr (kFixed) {
+            weigh_fixed(is_edge);
+          } else if constexpr (!kCap) {
             weigh(is_edge, both, plain);
           } else if (far) {
             weigh(is_edge, both, far_cap);
@@ -748,8 +773,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       t_item += it.n;
     }
     if (ok && t_item > 0 && t_item % kGroups == group) {   // the last item's output
-      float m, l;
-      if (!(ok = receive(kBarM, m_slot, t_item - 1, m) && receive(kBarL, l_slot, t_item - 1, l) &&
+      float m = 0.f, l;
+      if (!(ok = (kFixed || receive(kBarM, m_slot, t_item - 1, m)) && receive(kBarL, l_slot, t_item - 1, l) &&
                  epilogue(prev, gi - 1, m, l)))
         timeout = true;
     }
@@ -779,14 +804,14 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-template <bool kCap, bool kBias>
+template <bool kCap, bool kBias, bool kFixed = false>
 int launch_form(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                 const Params& prm, cudaStream_t stream) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(scored_prefill_kernel<kCap, kBias>,
+    if (cudaFuncSetAttribute(scored_prefill_kernel<kCap, kBias, kFixed>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes) != cudaSuccess)
       return PKV_ERR_LAUNCH;
@@ -795,7 +820,7 @@ int launch_form(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap&
   int sms = device_sm_count();
   if (sms <= 0) sms = 148;
   const int grid = prm.n_items < sms ? prm.n_items : sms;
-  scored_prefill_kernel<kCap, kBias><<<grid, kThreads, kSmemBytes, stream>>>(qm, km, vm, prm);
+  scored_prefill_kernel<kCap, kBias, kFixed><<<grid, kThreads, kSmemBytes, stream>>>(qm, km, vm, prm);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
@@ -855,6 +880,8 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   for (int k = 0; k < 5; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
     prm.poly[k] = static_cast<float>(t[k] * f);
   if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) prm.cap_x = INFINITY;
+  if (!bias && prm.cap_log2 <= kFixedCap)
+    return launch_form<true, false, true>(qm, km, vm, prm, stream);
   return bias ? launch_form<true, true>(qm, km, vm, prm, stream)
               : launch_form<true, false>(qm, km, vm, prm, stream);
 }

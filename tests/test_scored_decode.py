@@ -165,6 +165,15 @@ def test_large_scores():
 
 @gpu
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("softcap", [1e-3, 0.3, 70.0, 500.0, 1e4, 1e7])
+def test_caps_of_any_size(softcap, fp8):
+    b = Batch([40, 513, 1100], 8, 2, 710, fp8, spread=20.0)
+    b.check("cap", softcap=softcap)
+    b.check("cap", softcap=softcap, alibi_slopes=R.alibi(8), window=200)
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
 def test_no_options_equal_plain_attention(fp8):
     b = Batch([1, 300, 1000, 4100], 16, 8, 800, fp8)
     args = [x.to("cuda") for x in (b.q, b.kc, b.vc, b.tables, b.lens)]

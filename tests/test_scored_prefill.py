@@ -162,6 +162,43 @@ def test_large_scores():
 
 
 @gpu
+@pytest.mark.parametrize("softcap", [1e-3, 0.3, 69.0, 70.0, 500.0, 1e4, 1e7])
+def test_caps_of_any_size(softcap):
+    b = Batch([0, 100], [150, 300], 4, 2, 131, spread=20.0)
+    b.check("cap", softcap=softcap)
+    b.check("cap", softcap=softcap, alibi_slopes=R.alibi(4), window=200)
+
+
+@gpu
+@pytest.mark.parametrize("softcap", [0.0, 30.0, 69.0, 200.0])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_scores_all_of_one_sign(sign, softcap):
+    """Every score far below zero (or above): the whole row at one end of the cap."""
+    b = Batch([0, 130], [200, 260], 4, 2, 132)
+    b.kc.copy_(b.kc.float().abs())
+    b.q.copy_(sign * 4 * b.q.float().abs())
+    b.check("one sign", softcap=softcap)
+
+
+@gpu
+@pytest.mark.parametrize("opt", [{}, dict(softcap=300.0), dict(alibi=True), dict(window=300)])
+def test_maximum_that_keeps_rising(opt):
+    """Scores that grow by hundreds from tile to tile, so that the running maximum
+    moves at every one of them."""
+    opt = dict(opt)
+    if opt.pop("alibi", False):
+        opt["alibi_slopes"] = R.alibi(2)
+    b = Batch([0, 130], [700, 400], 2, 1, 133, spread=1.0)
+    b.q.copy_(b.q.float().abs())
+    for i, n in enumerate((700, 530)):
+        j = torch.arange(n)
+        slots = b.tables[i].long()[j // 256] * 256 + j % 256
+        rows = b.kc.view(-1, 1, 128)
+        rows[slots] = (rows[slots].float().abs() * (j[:, None, None] * 0.1)).to(torch.bfloat16)
+    b.check("rising", **opt)
+
+
+@gpu
 def test_no_options_equal_plain_attention():
     b = Batch([0, 300, 17], [260, 129, 1], 8, 2, 140)
     out, lse = b.run()
