@@ -10,6 +10,7 @@ if the shared library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -600,61 +601,60 @@ def paged_prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 
 
 class _Launch:
-    """Where a call runs: the device of its tensors, made current for the call,
-    and the given stream (a torch stream or a raw handle), or that device's
-    current one.  With a given stream, what the call allocates belongs to it.
-    `handle` is the stream to launch on."""
-
-    __slots__ = ("device", "stream", "handle", "_guards")
+    """Makes the device of a call's tensors current, and the given stream (a torch
+    stream or a raw handle), so that what the call allocates belongs to both."""
 
     def __init__(self, device: torch.device, stream):
-        self.device, self.stream, self._guards = device, stream, ()
+        if device.type != "cuda":
+            raise ValueError(f"the tensors must be on a CUDA device, not {device}")
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                      else torch.cuda.default_stream(device))
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self._guards = [torch.cuda.device(device)]
+        if stream is not None:
+            self._guards.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        guards = []
-        if self.device.index != torch.cuda.current_device():
-            guards.append(torch.cuda.device(self.device))
-        if self.stream is not None:
-            s = self.stream
-            if not isinstance(s, torch.cuda.Stream):
-                s = (torch.cuda.ExternalStream(int(s), device=self.device) if int(s)
-                     else torch.cuda.default_stream(self.device))
-            if s.device != self.device:
-                raise ValueError(f"stream is on {s.device}, the tensors on {self.device}")
-            guards.append(torch.cuda.stream(s))
-        for g in guards:
+        for g in self._guards:
             g.__enter__()
-        self._guards = tuple(reversed(guards))
-        self.handle = torch.cuda.current_stream().cuda_stream
-        return self
 
     def __exit__(self, *exc):
-        for g in self._guards:
+        for g in reversed(self._guards):
             g.__exit__(*exc)
         return False
 
-    def workspace(self, given: Optional[torch.Tensor], nbytes: int):
-        """(pointer, bytes) of the caller's workspace, or of one kept for this
-        stream (calls on one stream do not overlap).  A captured call needs the
-        caller's own: a later, larger call would free the kept one under the
-        graph."""
-        if given is not None:
-            if not isinstance(given, torch.Tensor) or given.device != self.device:
-                raise ValueError(f"workspace must be a tensor on {self.device}")
-            if not given.is_contiguous():
-                raise ValueError("workspace must be contiguous")
-            return given.data_ptr(), given.numel() * given.element_size()
-        if not nbytes:
-            return 0, 0
-        if torch.cuda.is_current_stream_capturing():
-            raise ValueError("a captured call needs a workspace of its own (zeroed, of "
-                             f"{nbytes} bytes)")
-        key = (self.device.index, self.handle)
-        ws = _stream_workspaces.get(key)
-        if ws is None or ws.numel() < nbytes:
-            ws = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            _stream_workspaces[key] = ws
-        return ws.data_ptr(), ws.numel()
+
+# The current device and its current stream as plain numbers (the public calls
+# build a stream object each time: 3 us of a small call's 15).
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _current_stream(device_index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def _workspace(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, handle: int):
+    """(pointer, bytes) of the caller's workspace, or of one kept for this stream
+    (calls on one stream do not overlap).  A captured call needs the caller's own: a
+    later, larger call would free the kept one under the graph."""
+    if given is not None:
+        _same_device(like.device, workspace=given)
+        if not given.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return given.data_ptr(), given.numel() * given.element_size()
+    if not nbytes:
+        return 0, 0
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError(f"a captured call needs a workspace of its own (zeroed, {nbytes} bytes)")
+    key = (like.get_device(), handle)
+    ws = _stream_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=like.device)
+        _stream_workspaces[key] = ws
+    return ws.data_ptr(), ws.numel()
 
 
 def _same_device(device: torch.device, **tensors):
@@ -663,34 +663,26 @@ def _same_device(device: torch.device, **tensors):
             raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor, fp8: bool):
+def _check_norm_rope(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                     k_weight, q_out, fp8):
+    """Raises what is wrong with the tensors of _norm_rope_store, by name."""
     NB, bs, Hkv, D = (_fp8_pool_dims if fp8 else _pool_dims)(k_cache, v_cache)
-    return NB, bs, Hkv, D
-
-
-def _norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
-                     k_weight, eps, interleaved, q_out, stream, scales):
-    fp8 = scales is not None
-    lib = load_library()
-    NB, bs, Hkv, D = _pools(k_cache, v_cache, fp8)
     _need(q, "q", torch.bfloat16, 3, contiguous=False)
     T, Hq = q.shape[0], q.shape[1]
     for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
         _need(t, name, torch.bfloat16, 3, contiguous=False)
-        if t.shape[0] != T or t.shape[1] != heads or t.shape[2] != D:
+        if tuple(t.shape) != (T, heads, D):
             raise ValueError(f"{name} must be [{T}, {heads}, {D}], got {tuple(t.shape)}")
         if T and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != D)):
             raise ValueError(f"{name} must have contiguous rows")
     _need(slot_mapping, "slot_mapping", torch.int32, 1)
-    if slot_mapping.shape[0] != T:
-        raise ValueError("slot_mapping and q disagree on T")
-    rotary = places = 0
     if cos_sin is not None:
         _need(cos_sin, "cos_sin", torch.float32, 2)
-        places, rotary = cos_sin.shape
         _need(positions, "positions", torch.int32, 1)
-        if positions.shape[0] != T:
-            raise ValueError("positions and q disagree on T")
+    for name, t in (("slot_mapping", slot_mapping),
+                    ("positions", positions if cos_sin is not None else None)):
+        if t is not None and t.shape[0] != T:
+            raise ValueError(f"{name} and q disagree on T")
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
         if t is not None:
             _need(t, name, torch.float32, 1)
@@ -701,24 +693,74 @@ def _norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin
         if q_out.shape != q.shape:
             raise ValueError("q_out and q differ in shape")
     _same_device(k_cache.device, q=q, k=k, v=v, v_cache=v_cache, slot_mapping=slot_mapping,
-                 positions=positions if rotary else None, cos_sin=cos_sin, q_weight=q_weight,
-                 k_weight=k_weight, q_out=q_out)
-    with _Launch(k_cache.device, stream) as at:
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=at.device)
-        # a single row's token stride says nothing (torch may give it any value)
-        strides = [t.stride(0) if T > 1 else t.shape[1] * D for t in (q, k, v)]
-        args = (q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *strides,
-                k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
-                positions.data_ptr() if rotary else None,
-                cos_sin.data_ptr() if rotary else None, places, rotary, 1 if interleaved else 0,
-                None if q_weight is None else q_weight.data_ptr(),
-                None if k_weight is None else k_weight.data_ptr(), eps, T, Hq, Hkv, D, bs, NB)
-        if fp8:
-            _check(lib.kv_cache_store_norm_rope_fp8(*args, scales[0], scales[1], at.handle),
-                   "kv_cache_store_norm_rope_fp8")
-        else:
-            _check(lib.kv_cache_store_norm_rope(*args, at.handle), "kv_cache_store_norm_rope")
+                 positions=positions if cos_sin is not None else None, cos_sin=cos_sin,
+                 q_weight=q_weight, k_weight=k_weight, q_out=q_out)
+
+
+def _norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                     k_weight, eps, interleaved, q_out, stream, scales):
+    lib = _lib or load_library()
+    bf16, f32 = torch.bfloat16, torch.float32
+    dtype = bf16 if scales is None else torch.uint8
+    fine = False
+    try:   # every check at once; _check_norm_rope says which one failed
+        NB, bs, Hkv, D = pool = k_cache.shape
+        T, Hq, _ = shape = q.shape
+        kv, row, one = (T, Hkv, D), (D,), (T,)
+        at = k_cache.get_device()
+        qs, ks, vs = q.stride(), k.stride(), v.stride()
+        fine = (
+            at >= 0 and shape == (T, Hq, D) and k.shape == kv and v.shape == kv
+            and v_cache.shape == pool and slot_mapping.shape == one
+            and k_cache.dtype is dtype and v_cache.dtype is dtype
+            and q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16
+            and slot_mapping.dtype is torch.int32
+            and qs[2] == 1 and ks[2] == 1 and vs[2] == 1
+            and (qs[1] == D or Hq == 1) and ((ks[1] == D and vs[1] == D) or Hkv == 1)
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and slot_mapping.is_contiguous()
+            and q.get_device() == at and k.get_device() == at and v.get_device() == at
+            and v_cache.get_device() == at and slot_mapping.get_device() == at
+            and (cos_sin is None or (
+                cos_sin.dtype is f32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()
+                and cos_sin.get_device() == at and positions.dtype is torch.int32
+                and positions.shape == one and positions.is_contiguous()
+                and positions.get_device() == at))
+            and (q_weight is None or (q_weight.dtype is f32 and q_weight.shape == row
+                                      and q_weight.is_contiguous()
+                                      and q_weight.get_device() == at))
+            and (k_weight is None or (k_weight.dtype is f32 and k_weight.shape == row
+                                      and k_weight.is_contiguous()
+                                      and k_weight.get_device() == at))
+            and (q_out is None or (q_out.dtype is bf16 and q_out.shape == shape
+                                   and q_out.is_contiguous() and q_out.get_device() == at)))
+    except (AttributeError, ValueError, TypeError):
+        pass
+    if not fine:
+        _check_norm_rope(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                         k_weight, q_out, scales is not None)
+    if stream is not None or at != _current_device():
+        with _Launch(k_cache.device, stream):
+            return _norm_rope_store(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin,
+                                    q_weight, k_weight, eps, interleaved, q_out, None, scales)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=bf16, device=q.device)
+    places, rotary = (0, 0) if cos_sin is None else cos_sin.shape
+    if T < 2:   # a single row's token stride says nothing (torch may give it any value)
+        qs, ks, vs = (Hq * D,), (Hkv * D,), (Hkv * D,)
+    args = (q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), qs[0], ks[0], vs[0],
+            k_cache.data_ptr(), v_cache.data_ptr(), slot_mapping.data_ptr(),
+            positions.data_ptr() if rotary else None, cos_sin.data_ptr() if rotary else None,
+            places, rotary, 1 if interleaved else 0,
+            None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), float(eps), T, Hq, Hkv, D, bs, NB)
+    if scales is None:
+        status = lib.kv_cache_store_norm_rope(*args, _current_stream(at))
+    else:
+        status = lib.kv_cache_store_norm_rope_fp8(*args, float(scales[0]), float(scales[1]),
+                                                  _current_stream(at))
+    if status != PKV_OK:
+        raise PkvError(status, "kv_cache_store_norm_rope" + ("" if scales is None else "_fp8"))
     return q_out
 
 
@@ -754,29 +796,41 @@ def kv_cache_store_norm_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
                             k_weight, eps, interleaved, q_out, stream, (k_scale, v_scale))
 
 
-def _score_options(rows: int, batch: int, Hq: int, softcap, alibi_slopes, window, first_keys,
-                   prefix_lens=None) -> ScoreOptions:
-    o = ScoreOptions(softcap, window)
-    if alibi_slopes is not None:
-        _need(alibi_slopes, "alibi_slopes", torch.float32, 1)
-        if alibi_slopes.shape[0] != Hq:
-            raise ValueError(f"alibi_slopes must be [{Hq}]")
-        o.alibi_slopes = alibi_slopes.data_ptr()
-    if first_keys is not None:
-        _need(first_keys, "first_keys", torch.int32, 1)
-        if first_keys.shape[0] != rows:
-            raise ValueError(f"first_keys must be [{rows}]")
-        o.first_keys = first_keys.data_ptr()
-    if prefix_lens is not None:
-        _need(prefix_lens, "prefix_lens", torch.int32, 1)
-        if prefix_lens.shape[0] != batch:
-            raise ValueError(f"prefix_lens must be [{batch}]")
-        o.prefix_lens = prefix_lens.data_ptr()
-    return o
+@functools.lru_cache(maxsize=256)
+def _scored_workspace_bytes(device_index, B, Hq, Hkv, D, maxblk, bs, window, num_splits) -> int:
+    return int(load_library().paged_decode_scored_workspace_bytes(B, Hq, Hkv, D, maxblk, bs,
+                                                                  window, num_splits))
 
 
-def _outputs(q: torch.Tensor, out, lse, want_lse: bool):
-    """Checks of a given out / lse, before anything is allocated."""
+def paged_decode_scored_workspace_bytes(B: int, Hq: int, Hkv: int, D: int,
+                                        max_blocks_per_seq: int, block_size: int = 256,
+                                        window: int = 0, num_splits: int = 0) -> int:
+    """Workspace of a scored decode call of these sizes on the current device."""
+    return int(load_library().paged_decode_scored_workspace_bytes(
+        B, Hq, Hkv, D, max_blocks_per_seq, block_size, window, num_splits))
+
+
+def _check_scored(q, k_cache, v_cache, block_tables, ints, rows, batch, alibi_slopes, first_keys,
+                  prefix_lens, out, lse, fp8):
+    """Raises what is wrong with the tensors of a scored call, by name."""
+    NB, bs, Hkv, D = (_fp8_pool_dims if fp8 else _pool_dims)(k_cache, v_cache)
+    _need(q, "q", torch.bfloat16, 3)
+    if q.shape[2] != D:
+        raise ValueError("q head_dim differs from the cache's")
+    _need(block_tables, "block_tables", torch.int32, 2)
+    if block_tables.shape[0] != batch:
+        raise ValueError(f"block_tables must have {batch} rows")
+    for name, (t, n) in ints.items():
+        _need(t, name, torch.int32, 1)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must be [{n}]")
+    for name, t, dtype, n in (("alibi_slopes", alibi_slopes, torch.float32, q.shape[1]),
+                              ("first_keys", first_keys, torch.int32, rows),
+                              ("prefix_lens", prefix_lens, torch.int32, batch)):
+        if t is not None:
+            _need(t, name, dtype, 1)
+            if t.shape[0] != n:
+                raise ValueError(f"{name} must be [{n}]")
     if out is not None:
         _need(out, "out", torch.bfloat16, 3)
         if out.shape != q.shape:
@@ -785,53 +839,91 @@ def _outputs(q: torch.Tensor, out, lse, want_lse: bool):
         _need(lse, "lse", torch.float32, 2)
         if lse.shape != q.shape[:2]:
             raise ValueError(f"lse must be {tuple(q.shape[:2])}")
+    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 alibi_slopes=alibi_slopes, first_keys=first_keys, prefix_lens=prefix_lens,
+                 out=out, lse=lse, **{name: t for name, (t, _) in ints.items()})
 
 
-def paged_decode_scored_workspace_bytes(B: int, Hq: int, Hkv: int, D: int,
-                                        max_blocks_per_seq: int, block_size: int = 256,
-                                        window: int = 0, num_splits: int = 0) -> int:
-    return int(load_library().paged_decode_scored_workspace_bytes(
-        B, Hq, Hkv, D, max_blocks_per_seq, block_size, window, num_splits))
+def _scored_fine(q, k_cache, v_cache, block_tables, lens, lens2, n_lens, rows, batch, alibi_slopes,
+                 first_keys, prefix_lens, out, lse, dtype) -> bool:
+    """Whether the tensors of a scored call pass every check (_check_scored says
+    which one failed)."""
+    i32 = torch.int32
+    try:
+        shape, pool = q.shape, k_cache.shape
+        at = q.get_device()
+
+        def vector(t, kind, n):
+            return (t.dtype is kind and t.shape == (n,) and t.is_contiguous()
+                    and t.get_device() == at)
+
+        return (
+            at >= 0 and len(shape) == 3 and len(pool) == 4 and shape[2] == pool[3]
+            and v_cache.shape == pool and k_cache.dtype is dtype and v_cache.dtype is dtype
+            and q.dtype is torch.bfloat16 and block_tables.dtype is i32
+            and block_tables.dim() == 2 and block_tables.shape[0] == batch
+            and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and block_tables.is_contiguous()
+            and k_cache.get_device() == at and v_cache.get_device() == at
+            and block_tables.get_device() == at
+            and vector(lens, i32, n_lens) and (lens2 is None or vector(lens2, i32, n_lens))
+            and (alibi_slopes is None or vector(alibi_slopes, torch.float32, shape[1]))
+            and (first_keys is None or vector(first_keys, i32, rows))
+            and (prefix_lens is None or vector(prefix_lens, i32, batch))
+            and (out is None or (out.dtype is torch.bfloat16 and out.shape == shape
+                                 and out.is_contiguous() and out.get_device() == at))
+            and (lse is None or (lse.dtype is torch.float32 and lse.shape == shape[:2]
+                                 and lse.is_contiguous() and lse.get_device() == at)))
+    except (AttributeError, ValueError, TypeError, IndexError):
+        return False
+
+
+def _score_options(softcap, alibi_slopes, window, first_keys, prefix_lens=None) -> ScoreOptions:
+    return ScoreOptions(float(softcap), int(window),
+                        None if alibi_slopes is None else alibi_slopes.data_ptr(),
+                        None if first_keys is None else first_keys.data_ptr(),
+                        None if prefix_lens is None else prefix_lens.data_ptr())
 
 
 def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scales, softcap,
                    alibi_slopes, window, first_keys, out, lse, workspace, num_splits, want_lse,
                    stream):
+    lib = _lib or load_library()
     fp8 = scales is not None
-    lib = load_library()
-    NB, bs, Hkv, D = _pools(k_cache, v_cache, fp8)
-    _need(q, "q", torch.bfloat16, 3)
-    B, Hq, Dq = q.shape
-    if Dq != D:
-        raise ValueError("q head_dim differs from the cache's")
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
+    B = q.shape[0]
+    if not _scored_fine(q, k_cache, v_cache, block_tables, context_lens, None, B, B, B,
+                        alibi_slopes, first_keys, None, out, lse,
+                        torch.uint8 if fp8 else torch.bfloat16):
+        _check_scored(q, k_cache, v_cache, block_tables, {"context_lens": (context_lens, B)}, B, B,
+                      alibi_slopes, first_keys, None, out, lse, fp8)
+    at = q.get_device()
+    if stream is not None or at != _current_device():
+        with _Launch(q.device, stream):
+            return _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scales,
+                                  softcap, alibi_slopes, window, first_keys, out, lse, workspace,
+                                  num_splits, want_lse, None)
+    Hq = q.shape[1]
+    NB, bs, Hkv, D = k_cache.shape
     maxblk = block_tables.shape[1]
-    if block_tables.shape[0] != B or context_lens.shape[0] != B:
-        raise ValueError("block_tables / context_lens batch differs from q")
-    options = _score_options(B, B, Hq, softcap, alibi_slopes, window, first_keys)
-    _outputs(q, out, lse, want_lse)
-    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 context_lens=context_lens, alibi_slopes=alibi_slopes, first_keys=first_keys,
-                 out=out, lse=lse)
-    with _Launch(q.device, stream) as at:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=at.device)
-        need = lib.paged_decode_scored_workspace_bytes(B, Hq, Hkv, D, maxblk, bs, window,
-                                                       num_splits)
-        ws, ws_bytes = at.workspace(workspace, need)
-        args = (out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
-                k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), maxblk,
-                context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, scale)
-        if fp8:
-            _check(lib.paged_decode_attention_scored_fp8(
-                *args, scales[0], scales[1], options, ws, ws_bytes, num_splits, at.handle),
-                "paged_decode_attention_scored_fp8")
-        else:
-            _check(lib.paged_decode_attention_scored(*args, options, ws, ws_bytes, num_splits,
-                                                     at.handle), "paged_decode_attention_scored")
+    handle = _current_stream(at)
+    num_splits = int(num_splits)
+    need = _scored_workspace_bytes(at, B, Hq, Hkv, D, maxblk, bs, int(window), num_splits)
+    ws, ws_bytes = _workspace(workspace, need, q, handle) if need or workspace is not None else (0, 0)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    args = (out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), maxblk,
+            context_lens.data_ptr(), B, Hq, Hkv, D, bs, NB, float(scale))
+    options = _score_options(softcap, alibi_slopes, window, first_keys)
+    if fp8:
+        status = lib.paged_decode_attention_scored_fp8(*args, float(scales[0]), float(scales[1]),
+                                                       options, ws, ws_bytes, num_splits, handle)
+    else:
+        status = lib.paged_decode_attention_scored(*args, options, ws, ws_bytes, num_splits, handle)
+    if status != PKV_OK:
+        raise PkvError(status, "paged_decode_attention_scored" + ("_fp8" if fp8 else ""))
     return out, lse
 
 
@@ -886,34 +978,35 @@ def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     (first_keys: int32, one per query row) and prefix_lens (int32 [B]): the first
     prefix_lens[b] tokens are visible to every row of sequence b.  Returns (out
     bf16 [sum Lq, Hq, D], lse fp32 [sum Lq, Hq] or None)."""
-    lib = load_library()
-    NB, bs, Hkv, D = _pool_dims(k_cache, v_cache)
-    _need(q, "q", torch.bfloat16, 3)
-    Nq, Hq, Dq = q.shape
-    if Dq != D:
-        raise ValueError("q head_dim differs from the cache's")
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
-    B = cu_seqlens_q.shape[0] - 1
-    if B < 0 or cu_seqlens_k.shape[0] != B + 1 or block_tables.shape[0] != B:
-        raise ValueError("cu_seqlens / block_tables batch sizes differ")
-    options = _score_options(Nq, B, Hq, softcap, alibi_slopes, window, first_keys, prefix_lens)
-    _outputs(q, out, lse, want_lse)
-    _same_device(q.device, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, alibi_slopes=alibi_slopes,
-                 first_keys=first_keys, prefix_lens=prefix_lens, out=out, lse=lse)
-    with _Launch(q.device, stream) as at:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and want_lse:
-            lse = torch.empty((Nq, Hq), dtype=torch.float32, device=at.device)
-        _check(lib.paged_prefill_attention_scored(
-            out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B,
-            Nq, max_seqlen_q, max_seqlen_k, Hq, Hkv, D, bs, NB, scale, options, at.handle),
-            "paged_prefill_attention_scored")
+    lib = _lib or load_library()
+    Nq = q.shape[0]
+    B = block_tables.shape[0]
+    if not _scored_fine(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, B + 1, Nq, B,
+                        alibi_slopes, first_keys, prefix_lens, out, lse, torch.bfloat16):
+        _check_scored(q, k_cache, v_cache, block_tables,
+                      {"cu_seqlens_q": (cu_seqlens_q, B + 1), "cu_seqlens_k": (cu_seqlens_k, B + 1)},
+                      Nq, B, alibi_slopes, first_keys, prefix_lens, out, lse, False)
+    at = q.get_device()
+    if stream is not None or at != _current_device():
+        with _Launch(q.device, stream):
+            return paged_prefill_attention_scored(
+                q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                max_seqlen_k, scale, softcap, alibi_slopes, window, first_keys, prefix_lens, out,
+                lse, want_lse)
+    Hq = q.shape[1]
+    NB, bs, Hkv, D = k_cache.shape
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty((Nq, Hq), dtype=torch.float32, device=q.device)
+    status = lib.paged_prefill_attention_scored(
+        out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Nq, int(max_seqlen_q),
+        int(max_seqlen_k), Hq, Hkv, D, bs, NB, float(scale), _score_options(softcap, alibi_slopes, window, first_keys,
+                                              prefix_lens), _current_stream(at))
+    if status != PKV_OK:
+        raise PkvError(status, "paged_prefill_attention_scored")
     return out, lse
 
 
