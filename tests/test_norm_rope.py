@@ -176,6 +176,21 @@ def test_zero_rows_and_tiny_eps():
 
 
 @gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_infinities_stay_in_their_pair(interleaved):
+    """Without a norm, an infinity reaches its rotated partner and nothing else."""
+    m = make(3, 4, 2, rotary=32, norm=False, packed=False, seed=16)
+    m["q"][0, 0, 5], m["q"][1, 1, 100], m["q"][2, 2, 40] = float("inf"), float("nan"), -float("inf")
+    q = call(m, interleaved=interleaved)[0].cpu().double()
+    want = R.norm_rope(m["q"], None, 0.0, m["positions"], m["cos_sin"], interleaved)
+    fine = torch.isfinite(want)
+    assert torch.equal(torch.isfinite(q), fine)
+    assert (~fine).sum().item() == 4
+    over = (q - want).abs()[fine] - 2.0 ** -8 * want.abs()[fine] - 2.0 ** -16
+    assert over.max().item() <= 0
+
+
+@gpu
 def test_bad_indices_are_reported_and_skipped():
     m = make(20, 6, 2, packed=False, seed=10)
     good = make(20, 6, 2, packed=False, seed=10)
