@@ -507,10 +507,10 @@ typedef struct pkv_score_options {
  * pkv_score_options.  Only the blocks that hold visible keys are read, so table
  * entries below them may be stale (blocks freed behind a window).  scale must be
  * finite and > 0, out must not overlap q, and the workspace size comes from
- * paged_decode_scored_workspace_bytes with the same arguments; everything else
- * as paged_decode_attention. */
+ * paged_decode_scored_workspace_bytes with the same arguments (fp8 != 0 for the
+ * E4M3 call); everything else as paged_decode_attention. */
 size_t paged_decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks_per_seq,
-                                           int block_size, int window, int num_splits);
+                                           int block_size, int window, int fp8, int num_splits);
 int paged_decode_attention_scored(void* out, float* lse, const void* q, const void* k_cache,
                                   const void* v_cache, const int32_t* block_tables,
                                   int max_blocks_per_seq, const int32_t* context_lens, int B,

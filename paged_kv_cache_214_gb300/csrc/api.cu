@@ -578,7 +578,7 @@ int decode_scored_entry(const DecodeArgs& a, const pkv_score_options* options, i
   if (overlap(a.out, bytes, a.q, bytes)) return PKV_ERR_ARG;
   DecodePlan plan;
   st = plan_decode_scored(a.B, a.Hq, a.Hkv, a.max_blocks_per_seq, opt.window, a.num_splits,
-                          device_sm_count(), &plan);
+                          a.fp8, device_sm_count(), &plan);
   if (st) return st;
   if (plan.workspace_bytes && (!a.workspace || a.workspace_bytes < plan.workspace_bytes ||
                                !aligned_to(a.workspace, 256)))
@@ -619,11 +619,11 @@ extern "C" int kv_cache_store_norm_rope_fp8(
 
 extern "C" size_t paged_decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D,
                                                       int max_blocks_per_seq, int block_size,
-                                                      int window, int num_splits) {
+                                                      int window, int fp8, int num_splits) {
   if (D != kHeadDim || block_size != kBlockSize || num_splits < 0) return 0;
   DecodePlan plan;
-  if (plan_decode_scored(B, Hq, Hkv, max_blocks_per_seq, window, num_splits, device_sm_count(),
-                         &plan))
+  if (plan_decode_scored(B, Hq, Hkv, max_blocks_per_seq, window, num_splits, fp8,
+                         device_sm_count(), &plan))
     return 0;
   return plan.workspace_bytes;
 }

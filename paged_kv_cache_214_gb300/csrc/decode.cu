@@ -11,6 +11,12 @@ int set_wait_hook_decode(unsigned long long limit_ns, int withhold_plus1) {
   return cudaMemcpyToSymbol(g_wait_hook, &h, sizeof h) == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
+size_t decode_partials_bytes(int B, int Hq, int num_splits) {
+  const size_t rows = static_cast<size_t>(B) * Hq * num_splits;
+  return kCounterRegion + align_up(rows * kHeadDim * sizeof(float), 256) +
+         align_up(rows * sizeof(float), 256);
+}
+
 int plan_decode(int B, int Hq, int Hkv, int max_blocks_per_seq, int num_splits,
                 int sm_count, int prefix_blocks, DecodePlan* plan) {
   if (B < 0 || Hq <= 0 || Hkv <= 0 || max_blocks_per_seq < 0 || prefix_blocks < 0 ||
@@ -98,10 +104,7 @@ int plan_decode(int B, int Hq, int Hkv, int max_blocks_per_seq, int num_splits,
   } else {
     if (static_cast<int64_t>(B) * kv_groups * plan->head_groups > kMaxCounters)
       return PKV_ERR_SHAPE;
-    const size_t rows = static_cast<size_t>(B) * Hq * S;
-    size_t bytes = kCounterRegion;
-    bytes += align_up(rows * kHeadDim * sizeof(float), 256);
-    bytes += align_up(rows * sizeof(float), 256);
+    size_t bytes = decode_partials_bytes(B, Hq, S);
     if (prefix_blocks > 0) {
       plan->prefix_offset = bytes;
       const size_t prow = static_cast<size_t>(B) * Hq * plan->prefix_splits;

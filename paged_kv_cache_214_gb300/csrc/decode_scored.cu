@@ -22,18 +22,51 @@ int set_wait_hook_decode_scored(unsigned long long limit_ns, int withhold_plus1)
 }
 
 int plan_decode_scored(int B, int Hq, int Hkv, int max_blocks_per_seq, int window, int num_splits,
-                       int sm_count, DecodePlan* plan) {
+                       int fp8, int sm_count, DecodePlan* plan) {
   if (B < 0 || window < 0 || max_blocks_per_seq < 0) return PKV_ERR_ARG;
   int blocks = max_blocks_per_seq;
-  if (window > 0) {
+  const bool bounded = window > 0 && window <= static_cast<int64_t>(blocks) * kBlockSize;
+  if (bounded) {
     // the window's tokens and up to a block before them
-    const int64_t touched = (static_cast<int64_t>(window) + 2 * kBlockSize - 2) / kBlockSize;
-    if (touched < blocks) blocks = static_cast<int>(touched);
+    const int touched = (window + 2 * kBlockSize - 2) / kBlockSize;
+    if (touched < blocks) blocks = touched;
   }
   const int st = plan_decode(B, Hq, Hkv, blocks, num_splits, sm_count, 0, plan);
   if (st) return st;
+  const int64_t row_units = static_cast<int64_t>(Hkv) * plan->head_groups;   // of a sequence
   // the launch grid: (splits, kv heads x head groups, sequences)
-  if (B > 65535 || static_cast<int64_t>(Hkv) * plan->head_groups > 65535) return PKV_ERR_SHAPE;
+  if (B > 65535 || row_units > 65535) return PKV_ERR_SHAPE;
+  if (!bounded || num_splits > 0 || B == 0) return PKV_OK;
+
+  // Every context has about the window's tokens, so that equal ranges of 64-token
+  // tiles are balanced, and few of them do: ranges to merge cost about 8 us more
+  // than one (partials written, a ticket, partials read), which is a chain of 11
+  // tiles (0.7 us a tile and block, half that with two consumer groups) unless the
+  // copy bandwidth is the limit (5 ns a tile of every block, E4M3 3 ns).  One range
+  // while that chain is the shorter, else ranges for one wave of two blocks an SM.
+  // Measured, one range against three: 64 sequences of 8 kv heads and a window of
+  // 1000 tokens 50 and 62 us; 16 sequences and 4096 tokens over E4M3 46 and 34 us.
+  const int64_t units = row_units * B;
+  const int64_t sms = sm_count > 0 ? sm_count : 148;
+  const int64_t tiles = (window - 1) / kTile + 2;   // that the window can touch
+  const bool two_groups = !fp8 && units <= sms;
+  const int64_t chain_ns = two_groups ? 350 : 700, copy_ns = fp8 ? 3 : 5;
+  int64_t S = 1;
+  if (units < 2 * sms && tiles * (chain_ns - copy_ns * units) > 8000)
+    S = (2 * sms + units - 1) / units;
+  if (S > tiles) S = tiles;
+  constexpr int kMostTiles = (kMaxSplitBlocks - 2) * (kBlockSize / kTile);   // block ids of a range
+  int per = static_cast<int>((tiles + S - 1) / S);
+  if (per > kMostTiles) per = kMostTiles;
+  // (a range of whole blocks would begin at a block, not at the window's tile)
+  if (per % (kBlockSize / kTile) == 0) per = per < kMostTiles ? per + 1 : per - 1;
+  S = (tiles + per - 1) / per;
+  if (S > kMaxSplits) return PKV_OK;   // plan_decode's ranges are longer
+  if (S > 1 && units > kMaxCounters) return PKV_ERR_SHAPE;
+  plan->split_tokens = per * kTile;
+  plan->num_splits = static_cast<int>(S);
+  plan->consumer_groups = S == 1 && two_groups ? 2 : 1;
+  plan->workspace_bytes = S > 1 ? decode_partials_bytes(B, Hq, plan->num_splits) : 0;
   return PKV_OK;
 }
 

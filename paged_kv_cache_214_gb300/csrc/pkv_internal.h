@@ -131,9 +131,12 @@ struct DecodePlan {
 int plan_decode(int B, int Hq, int Hkv, int max_blocks_per_seq, int num_splits,
                 int sm_count, int prefix_blocks, DecodePlan* plan);
 
+// Workspace of split partials: arrival counters, [B*Hq, S, 128] outputs and
+// [B*Hq, S] log2-sum-exps.
+size_t decode_partials_bytes(int B, int Hq, int num_splits);
 // The same for scored decode: window > 0 bounds the blocks a sequence needs.
 int plan_decode_scored(int B, int Hq, int Hkv, int max_blocks_per_seq, int window, int num_splits,
-                       int sm_count, DecodePlan* plan);
+                       int fp8, int sm_count, DecodePlan* plan);
 int launch_decode_scored(const DecodeArgs& a, const pkv_score_options& opt, const DecodePlan& plan,
                          unsigned* err, cudaStream_t stream);
 

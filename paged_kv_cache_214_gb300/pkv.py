@@ -115,7 +115,7 @@ def load_library(path: str = LIB_PATH):
         lib.kv_cache_store_norm_rope.restype = i32
         lib.kv_cache_store_norm_rope_fp8.argtypes = [*store, f32, f32, P]
         lib.kv_cache_store_norm_rope_fp8.restype = i32
-        lib.paged_decode_scored_workspace_bytes.argtypes = [i32] * 8
+        lib.paged_decode_scored_workspace_bytes.argtypes = [i32] * 9
         lib.paged_decode_scored_workspace_bytes.restype = sz
         decode = [P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i64, f32]
         lib.paged_decode_attention_scored.argtypes = [*decode, opt, P, sz, i32, P]
@@ -797,17 +797,19 @@ def kv_cache_store_norm_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
 
 
 @functools.lru_cache(maxsize=256)
-def _scored_workspace_bytes(device_index, B, Hq, Hkv, D, maxblk, bs, window, num_splits) -> int:
+def _scored_workspace_bytes(device_index, B, Hq, Hkv, D, maxblk, bs, window, fp8,
+                            num_splits) -> int:
     return int(load_library().paged_decode_scored_workspace_bytes(B, Hq, Hkv, D, maxblk, bs,
-                                                                  window, num_splits))
+                                                                  window, fp8, num_splits))
 
 
 def paged_decode_scored_workspace_bytes(B: int, Hq: int, Hkv: int, D: int,
                                         max_blocks_per_seq: int, block_size: int = 256,
-                                        window: int = 0, num_splits: int = 0) -> int:
+                                        window: int = 0, num_splits: int = 0,
+                                        fp8: bool = False) -> int:
     """Workspace of a scored decode call of these sizes on the current device."""
     return int(load_library().paged_decode_scored_workspace_bytes(
-        B, Hq, Hkv, D, max_blocks_per_seq, block_size, window, num_splits))
+        B, Hq, Hkv, D, max_blocks_per_seq, block_size, window, int(fp8), num_splits))
 
 
 def _check_scored(q, k_cache, v_cache, block_tables, ints, rows, batch, alibi_slopes, first_keys,
@@ -907,7 +909,8 @@ def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scale
     maxblk = block_tables.shape[1]
     handle = _current_stream(at)
     num_splits = int(num_splits)
-    need = _scored_workspace_bytes(at, B, Hq, Hkv, D, maxblk, bs, int(window), num_splits)
+    need = _scored_workspace_bytes(at, B, Hq, Hkv, D, maxblk, bs, int(window), int(fp8),
+                                   num_splits)
     ws, ws_bytes = _workspace(workspace, need, q, handle) if need or workspace is not None else (0, 0)
     if out is None:
         out = torch.empty_like(q)
