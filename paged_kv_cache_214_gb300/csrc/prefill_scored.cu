@@ -502,6 +502,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     };
 
     Item prev = {};
+    uint32_t ph = 0;          // phase of the group's S buffer and V stage
     int gi = 0, t_item = 0;   // items, and the running count of the item's first tile
     for (; ok; ++gi) {
       Item it;
@@ -518,25 +519,41 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
 
       int kt = group - t_item % kGroups;
       if (kt < 0) kt += kGroups;
-      for (; kt < it.n; kt += kGroups) {
+      const unsigned span = lo > hi ? 0u : static_cast<unsigned>(hi - lo);
+      for (; kt < it.n; kt += kGroups, ph ^= 1u) {
         const int t = t_item + kt;
-        const uint32_t ph = (t / kGroups) & 1;   // of the group's S buffer and V stage
-        if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
         if (!(ok = warp_wait(bar(kBarSFull + group), ph))) { timeout = true; break; }
         tc_fence_after();
         const int tile = (it.kt0 + kt) * kN;
         // the row's keys within the tile: c with c - c_lo <= span, unsigned
         const int c_lo = lo > hi ? 1 << 30 : lo - tile;
-        const unsigned span = lo > hi ? 0u : static_cast<unsigned>(hi - lo);
-        const bool edge = __any_sync(kFull, c_lo > 0 || c_lo + static_cast<int64_t>(span) < kN - 1);
+        const bool edge = __any_sync(kFull, c_lo > 0 || hi - tile < kN - 1);
         auto hidden = [&](int c) { return static_cast<unsigned>(c - c_lo) > span; };
+        // How the warp's rows see 32 keys from c0 on: -1 not at all, 0 wholly, 1 in
+        // part.  (Of a tile on the diagonal or at a window's end a warp sees about
+        // one chunk in part, and need not look at those it does not see.)
+        const int c_hi = lo > hi ? -1 : min(hi - tile, kN);
+        auto view = [&](auto is_edge, int c0) -> int {
+          if constexpr (is_edge) {
+            if (!__any_sync(kFull, c_lo < c0 + 32 && c_hi >= c0)) return -1;
+            return __any_sync(kFull, c_lo > c0 || c_hi < c0 + 31) ? 1 : 0;
+          }
+          return 0;
+        };
+        auto by_edge = [&](auto body) {
+          if (edge)
+            body(std::true_type{});
+          else
+            body(std::false_type{});
+        };
         // Biased: -slope |pos - j| = slope c + slope (tile - pos) for key j = tile + c
         // up to the row's own position; the second part is a constant of row and
         // tile, off.  Past that position (a two-way prefix) it is 2 slope (c - past)
         // less, past = pos - tile.
         const float past = static_cast<float>(pos - tile);
         const float off = kBias ? -slope * past : 0.f;
-        const bool two_way = kBias && it.prefix > 0;
+        const bool two_way =
+            kBias && it.prefix > 0 && __any_sync(kFull, hi > pos && tile + kN - 1 > pos);
         auto bias = [&](auto both, f32x2 c, f32x2 add) {
           f32x2 b = fma2(c, slope2, add);
           if constexpr (both)
@@ -572,8 +589,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // First pass: the row's maximum.  Unbiased: of the products, as the cap is
         // increasing.  Biased: of the scores less `off`.
         float mx = -INFINITY;
-        auto chunk_max = [&](const uint32_t (&r)[32], int c0) {
-          if (edge) {
+        auto chunk_max = [&](const uint32_t (&r)[32], int c0, int seen) {
+          if (seen == 1) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!hidden(c0 + c)) mx = fmaxf(mx, __uint_as_float(r[c]));
@@ -590,20 +607,26 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
             for (int c = 0; c < 32; c += 2)
               big = absmax3(big, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
           };
+          by_edge([&](auto is_edge) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < kN; c0 += 32) {
-            tmem_ld32x32_x32(s_col + c0, r0);
-            tmem_wait_ld(r0);
-            if constexpr (kCap) chunk_big(r0);
-            if constexpr (!kBias) chunk_max(r0, c0);
-          }
+            for (int c0 = 0; c0 < kN; c0 += 32) {
+              const int seen = view(is_edge, c0);
+              if (seen < 0) continue;
+              tmem_ld32x32_x32(s_col + c0, r0);
+              tmem_wait_ld(r0);
+              if constexpr (kCap) chunk_big(r0);
+              if constexpr (!kBias) chunk_max(r0, c0, seen);
+            }
+          });
           if constexpr (kCap) far = __any_sync(kFull, !(big * p.cap_x <= kTanhPoly));
         }
         if constexpr (kBias) {
           auto scan = [&](auto both, auto score) {
-            f32x2 c2 = pack2(0.f, 1.f);
 #pragma unroll 1
             for (int c0 = 0; c0 < kN; c0 += 32) {
+              const int seen = edge ? view(std::true_type{}, c0) : 0;
+              if (seen < 0) continue;
+              f32x2 c2 = pack2(static_cast<float>(c0), static_cast<float>(c0 + 1));
               tmem_ld32x32_x32(s_col + c0, r0);
               tmem_wait_ld(r0);
 #pragma unroll
@@ -614,7 +637,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                 r0[c] = __float_as_uint(lo2(v));
                 r0[c + 1] = __float_as_uint(hi2(v));
               }
-              chunk_max(r0, c0);
+              chunk_max(r0, c0, seen);
             }
           };
           auto scan_with = [&](auto both) {
@@ -671,9 +694,10 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         const float base = m == -INFINITY ? 0.f : off - m;
         const f32x2 base2 = pack2(base, base);
         f32x2 sum2 = pack2(0.f, 0.f);
-        f32x2 c2 = pack2(0.f, 1.f);   // (biased) the pair's keys within the tile
         auto chunk = [&](auto is_edge, auto both, auto score, int c0) {
           uint32_t pk[16];
+          // (biased) the pair's keys within the tile
+          f32x2 c2 = pack2(static_cast<float>(c0), static_cast<float>(c0 + 1));
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             f32x2 add = base2;
@@ -692,48 +716,50 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           }
           tmem_st32x32_x16(s_col + c0 / 2, pk);
         };
-        auto weigh = [&](auto is_edge, auto both, auto score) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < kN; c0 += 32) {
-            tmem_ld32x32_x32(s_col + c0, r0);
-            tmem_wait_ld(r0);
-            chunk(is_edge, both, score, c0);
-          }
+        auto chunk_as = [&](auto is_edge, int seen, auto both, auto score, int c0) {
+          if (is_edge && seen)
+            chunk(std::true_type{}, both, score, c0);
+          else
+            chunk(std::false_type{}, both, score, c0);
         };
-        auto weigh_fixed = [&](auto is_edge) {
+        by_edge([&](auto is_edge) {
 #pragma unroll 1
           for (int c0 = 0; c0 < kN; c0 += 32) {
-            tmem_ld32x32_x32(s_col + c0, r0);
-            tmem_wait_ld(r0);
-            float big = 0.f, big2 = 0.f;
-#pragma unroll
-            for (int c = 0; c < 32; c += 4) {
-              big = absmax3(big, __uint_as_float(r0[c]), __uint_as_float(r0[c + 1]));
-              big2 = absmax3(big2, __uint_as_float(r0[c + 2]), __uint_as_float(r0[c + 3]));
+            const int seen = view(is_edge, c0);
+            if (seen < 0) {
+              uint32_t none[16] = {};
+              tmem_st32x32_x16(s_col + c0 / 2, none);
+              continue;
             }
-            if (__any_sync(kFull, !(fmaxf(big, big2) * p.cap_x <= kTanhPoly)))
-              chunk(is_edge, std::false_type{}, far_cap, c0);
-            else
-              chunk(is_edge, std::false_type{}, near_cap, c0);
+            tmem_ld32x32_x32(s_col + c0, r0);
+            tmem_wait_ld(r0);
+            constexpr std::false_type one_way{};
+            if constexpr (kFixed) {
+              float big = 0.f, big2 = 0.f;
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                big = absmax3(big, __uint_as_float(r0[c]), __uint_as_float(r0[c + 1]));
+                big2 = absmax3(big2, __uint_as_float(r0[c + 2]), __uint_as_float(r0[c + 3]));
+              }
+              far = __any_sync(kFull, !(fmaxf(big, big2) * p.cap_x <= kTanhPoly));
+            }
+            if (two_way) {
+              constexpr std::integral_constant<bool, kBias> both{};
+              if (!kCap)
+                chunk(std::true_type{}, both, plain, c0);
+              else if (far)
+                chunk(std::true_type{}, both, far_cap, c0);
+              else
+                chunk(std::true_type{}, both, near_cap, c0);
+            } else if (!kCap) {
+              chunk_as(is_edge, seen, one_way, plain, c0);
+            } else if (far) {
+              chunk_as(is_edge, seen, one_way, far_cap, c0);
+            } else {
+              chunk_as(is_edge, seen, one_way, near_cap, c0);
+            }
           }
-        };
-        auto weigh_with = [&](auto is_edge, auto both) {
-          if constexpr (kFixed) {
-            weigh_fixed(is_edge);
-          } else if constexpr (!kCap) {
-            weigh(is_edge, both, plain);
-          } else if (far) {
-            weigh(is_edge, both, far_cap);
-          } else {
-            weigh(is_edge, both, near_cap);
-          }
-        };
-        if (two_way)
-          weigh_with(std::true_type{}, std::integral_constant<bool, kBias>{});
-        else if (edge)
-          weigh_with(std::true_type{}, std::false_type{});
-        else
-          weigh_with(std::false_type{}, std::false_type{});
+        });
 
         // keys outside [vlo, vhi]: zero their V rows so that 0 * (stale data)
         // cannot put a NaN into O (the group's thread s clears row s)
