@@ -46,6 +46,19 @@
 namespace pkv {
 namespace {
 
+// A bounded wait with every lane of the warp; the result is the same for all
+// lanes.  What follows a first unsuccessful try is out of line: the instruction
+// fetch is a limit of the softmax loops, and with every wait's loop inline around
+// them they ran 1 to 5% slower.
+__device__ __noinline__ bool slow_wait(uint32_t bar, uint32_t parity) {
+  return mbar_wait(bar, parity);
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = slow_wait(bar, parity);
+  return __all_sync(kFull, ok);
+}
+
 constexpr int kM = 128;   // query rows per tile
 constexpr int kN = 128;   // keys per tile
 constexpr int kGroups = 3;                 // softmax groups of four warps
@@ -254,7 +267,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   // false: a wait ran out.
   auto take_item = [&](int gi, Item& it) -> bool {
     const int slot = gi % kRing;
-    if (!warp_wait(bar(kBarItemFull + slot), (gi / kRing) & 1)) return false;
+    if (!wait(bar(kBarItemFull + slot), (gi / kRing) & 1)) return false;
     it = *reinterpret_cast<const Item*>(smem + kOffItems + slot * kItemBytes);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarItemEmpty + slot));
@@ -279,7 +292,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           if (idx < p.n_items) it = get_item(p, idx, lane);
         }
         const int slot = gi % kRing;
-        if (gi >= kRing && !warp_wait(bar(kBarItemEmpty + slot), (gi / kRing - 1) & 1)) {
+        if (gi >= kRing && !wait(bar(kBarItemEmpty + slot), (gi / kRing - 1) & 1)) {
           ok = false;
           timeout = true;
           break;
@@ -301,7 +314,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           const int id = it.vlo > it.vhi
                              ? 0 : ids.get(table, p.maxblk, gkt >> 1, lane, p.num_blocks, p.err);
           const int at = id * kBlockSize + (gkt & 1) * kN;
-          if (gk >= kKStages && !warp_wait(bar(kBarKEmpty + rk.idx), rk.ph ^ 1u)) {
+          if (gk >= kKStages && !wait(bar(kBarKEmpty + rk.idx), rk.ph ^ 1u)) {
             ok = false;
             timeout = true;
             break;
@@ -318,7 +331,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                         bar(kBarKFull + rk.idx), (lane & 1) * 64, it.kvh, at);
           __syncwarp();
           if (kt == 0) {
-            if (gi >= 1 && !warp_wait(bar(kBarQEmpty), (gi - 1) & 1)) {
+            if (gi >= 1 && !wait(bar(kBarQEmpty), (gi - 1) & 1)) {
               ok = false;
               timeout = true;
               break;
@@ -354,7 +367,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           const int id = it.vlo > it.vhi
                              ? 0 : ids.get(table, p.maxblk, gkt >> 1, lane, p.num_blocks, p.err);
           const int at = id * kBlockSize + (gkt & 1) * kN;
-          if (gk >= kVStages && !warp_wait(bar(kBarVEmpty + rv.idx), rv.ph ^ 1u)) {
+          if (gk >= kVStages && !wait(bar(kBarVEmpty + rv.idx), rv.ph ^ 1u)) {
             ok = false;
             timeout = true;
             break;
@@ -381,14 +394,14 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         Item it;
         if (!take_item(gi, it)) { ok = false; timeout = true; break; }
         if (it.n == 0) break;
-        if (!warp_wait(bar(kBarQFull), gi & 1)) { ok = false; timeout = true; break; }
+        if (!wait(bar(kBarQFull), gi & 1)) { ok = false; timeout = true; break; }
         const uint32_t q_s = sbase + kOffQ;
         for (int kt = 0; kt < it.n; ++kt, ++gk, sb.next(), rk.next()) {
           if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
           // K here, and the S buffer free: the PV that read P from it (three
           // tiles back) is done
-          if (!warp_wait(bar(kBarKFull + rk.idx), rk.ph) ||
-              (gk >= kSBufs && !warp_wait(bar(kBarPVDone + sb.idx), sb.ph ^ 1u))) {
+          if (!wait(bar(kBarKFull + rk.idx), rk.ph) ||
+              (gk >= kSBufs && !wait(bar(kBarPVDone + sb.idx), sb.ph ^ 1u))) {
             ok = false;
             timeout = true;
             break;
@@ -410,7 +423,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       }
       // every MMA this warp issued has completed once this arrives
       umma_commit_warp(bar(kBarDrainS));
-      (void)warp_wait(bar(kBarDrainS), 0);
+      (void)wait(bar(kBarDrainS), 0);
     } else {
       // ---------------------------------------------------------- MMA: O += P V
       constexpr uint32_t idesc_o = idesc_bf16_f32(kM, kHeadDim, 1);  // B = V, MN-major
@@ -423,8 +436,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         if (it.n == 0) break;
         for (int kt = 0; kt < it.n; ++kt, sb.next(), rv.next()) {
           if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
-          if (!warp_wait(bar(kBarVFull + rv.idx), rv.ph) ||
-              !warp_wait(bar(kBarPFull + sb.idx), sb.ph)) {
+          if (!wait(bar(kBarVFull + rv.idx), rv.ph) ||
+              !wait(bar(kBarPFull + sb.idx), sb.ph)) {
             ok = false;
             timeout = true;
             break;
@@ -446,7 +459,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         umma_commit_warp(bar(kBarOFull));
       }
       umma_commit_warp(bar(kBarDrainPV));
-      (void)warp_wait(bar(kBarDrainPV), 0);
+      (void)wait(bar(kBarDrainPV), 0);
     }
     if (timeout && lane == 0) record_error(p.err, kErrTimeout);
     if (!ok && lane == 0) flags[0] = 1;
@@ -471,13 +484,13 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       if (lane == 0) mbar_arrive(bar(first_bar + (t & 1) * 4 + quarter));
     };
     auto receive = [&](int first_bar, const float* slot, int t, float& v) -> bool {
-      if (!warp_wait(bar(first_bar + (t & 1) * 4 + quarter), (t >> 1) & 1)) return false;
+      if (!wait(bar(first_bar + (t & 1) * 4 + quarter), (t >> 1) & 1)) return false;
       v = *const_cast<const volatile float*>(slot + (t & 1) * kM);
       return true;
     };
     // Output of finished item number `done` (its m and l): O / l, row by row.
     auto epilogue = [&](const Item& e, int done, float m, float l) -> bool {
-      if (!warp_wait(bar(kBarOFull), done & 1)) return false;
+      if (!wait(bar(kBarOFull), done & 1)) return false;
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;   // a row without keys: 0 and -inf
       const bool valid = row < e.rows;
@@ -522,7 +535,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       const unsigned span = lo > hi ? 0u : static_cast<unsigned>(hi - lo);
       for (; kt < it.n; kt += kGroups, ph ^= 1u) {
         const int t = t_item + kt;
-        if (!(ok = warp_wait(bar(kBarSFull + group), ph))) { timeout = true; break; }
+        if (!(ok = wait(bar(kBarSFull + group), ph))) { timeout = true; break; }
         tc_fence_after();
         const int tile = (it.kt0 + kt) * kN;
         // the row's keys within the tile: c with c - c_lo <= span, unsigned
@@ -643,7 +656,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           auto scan_with = [&](auto both) {
             if (!kCap)
               scan(both, plain);
-            else if (far)
+            else if (__builtin_expect(far, 0))
               scan(both, far_cap);
             else
               scan(both, near_cap);
@@ -671,7 +684,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           // (a row without keys so far has O = 0 at any m)
           if (__any_sync(kFull, need && m_before > -INFINITY)) {
             // the previous tile's PV must have finished accumulating into O
-            if (!(ok = warp_wait(bar(kBarPVDone + (t - 1) % kSBufs), ((t - 1) / kSBufs) & 1))) {
+            if (!(ok = wait(bar(kBarPVDone + (t - 1) % kSBufs), ((t - 1) / kSBufs) & 1))) {
               timeout = true;
               break;
             }
@@ -747,13 +760,13 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
               constexpr std::integral_constant<bool, kBias> both{};
               if (!kCap)
                 chunk(std::true_type{}, both, plain, c0);
-              else if (far)
+              else if (__builtin_expect(far, 0))
                 chunk(std::true_type{}, both, far_cap, c0);
               else
                 chunk(std::true_type{}, both, near_cap, c0);
             } else if (!kCap) {
               chunk_as(is_edge, seen, one_way, plain, c0);
-            } else if (far) {
+            } else if (__builtin_expect(far, 0)) {
               chunk_as(is_edge, seen, one_way, far_cap, c0);
             } else {
               chunk_as(is_edge, seen, one_way, near_cap, c0);
@@ -764,7 +777,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // keys outside [vlo, vhi]: zero their V rows so that 0 * (stale data)
         // cannot put a NaN into O (the group's thread s clears row s)
         if ((kt == 0 && tile < it.vlo) || (kt == it.n - 1 && tile + kN - 1 > it.vhi)) {
-          if (!(ok = warp_wait(bar(kBarVFull + group), ph))) { timeout = true; break; }
+          if (!(ok = wait(bar(kBarVFull + group), ph))) { timeout = true; break; }
           if (tile + row < it.vlo || tile + row > it.vhi) {
             const uint4 zero = make_uint4(0, 0, 0, 0);
             const uint32_t vrow = sbase + kOffV + group * kTile + row * 128;
@@ -815,13 +828,13 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   if (flags[0] && tid == kQKWarp * 32) {
     const int kin = flags[1], qin = flags[3];
     for (int x = max(0, kin - kKStages); x < kin; ++x)
-      (void)mbar_wait(bar(kBarKFull + x % kKStages), (x / kKStages) & 1);
-    if (qin > 0) (void)mbar_wait(bar(kBarQFull), (qin - 1) & 1);
+      (void)slow_wait(bar(kBarKFull + x % kKStages), (x / kKStages) & 1);
+    if (qin > 0) (void)slow_wait(bar(kBarQFull), (qin - 1) & 1);
   }
   if (flags[0] && tid == kVWarp * 32) {
     const int vin = flags[2];
     for (int x = max(0, vin - kVStages); x < vin; ++x)
-      (void)mbar_wait(bar(kBarVFull + x % kVStages), (x / kVStages) & 1);
+      (void)slow_wait(bar(kBarVFull + x % kVStages), (x / kVStages) & 1);
   }
   __syncthreads();
   if (warp == kSWarp) {
