@@ -81,7 +81,9 @@ constexpr int kOffM = kOffV + kVStages * kTile;       // m(t): [t & 1][row] fp32
 constexpr int kOffL = kOffM + 2 * kM * 4;             // l(t): [t & 1][row] fp32
 constexpr int kOffItems = kOffL + 2 * kM * 4;         // kRing descriptors
 constexpr int kItemBytes = 48;
-constexpr int kOffBars = kOffItems + kRing * kItemBytes;
+constexpr int kOffAnswer = kOffItems + kRing * kItemBytes;
+constexpr int kOffBars = kOffAnswer + 16;
+static_assert(kOffAnswer % 16 == 0, "answer alignment");
 // barriers
 constexpr int kBarQFull = 0;
 constexpr int kBarQEmpty = 1;
@@ -99,7 +101,8 @@ constexpr int kBarItemFull = kBarDrainPV + 1;      // [descriptor]
 constexpr int kBarItemEmpty = kBarItemFull + kRing;   // [descriptor], every other warp
 constexpr int kBarM = kBarItemEmpty + kRing;       // m(t) is there: [t & 1][row / 32]
 constexpr int kBarL = kBarM + 8;                   // l(t) is there: [t & 1][row / 32]
-constexpr int kNumBars = kBarL + 8;
+constexpr int kBarNext = kBarL + 8;                // the next item's answer is there
+constexpr int kNumBars = kBarNext + 1;
 constexpr int kOffTmem = kOffBars + kNumBars * 8;
 constexpr int kOffFlags = kOffTmem + 8;
 constexpr int kSmemBytes = kOffFlags + 16;
@@ -129,7 +132,6 @@ struct Params {
   unsigned* err;
   int B, Hq, Hkv, maxblk, max_q, max_k, window;
   int n_qt;          // ceil(max_q / 128)
-  int n_items;
   int64_t num_blocks, total_q;
   float scale_log2;  // raw product -> log2 units; capped: -> 2 log2(e) s / c
   float cap_log2;    // the cap in log2 units
@@ -205,12 +207,28 @@ __device__ __forceinline__ Item get_item(const Params& p, int idx, int lane) {
   return it;
 }
 
-// Item of round k for this block: rounds alternate direction so that every
-// block gets a mix of heavy and light items.
-__device__ __forceinline__ int item_index(int k) {
-  const int c = (k & 1) ? static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)
-                        : static_cast<int>(blockIdx.x);
-  return k * static_cast<int>(gridDim.x) + c;
+// The grid has one block for each item, and as many run as there are SMs: a
+// running block takes the place of one that has not started yet (a cluster launch
+// control request, answered in 16 bytes of shared memory) until none is left.
+__device__ __forceinline__ void request_block(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+      ::"r"(answer), "r"(bar) : "memory");
+}
+// Index of the block whose place the answer gives, -1 if none was left.
+__device__ __forceinline__ int taken_block(uint32_t answer) {
+  int idx;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t.reg .b32 x, y, z, w;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.b32 x, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {x, y, z, w}, a;\n\t"
+      "mov.b32 %0, x;\n\t}"
+      : "=r"(idx)
+      : "r"(answer)
+      : "memory");
+  return idx;
 }
 
 // kCap: capped scores; kBias: biased ones; kFixed: capped by at most kFixedCap and
@@ -280,17 +298,45 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       // ---------------------------------------------------------- items, K and Q
       // An item's Q goes into the single Q buffer right after its first K tile
       // has been issued, once the S MMAs of the previous item are done with it.
-      const int n_rounds = (p.n_items + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
-      int gk = 0, round = 0;
+      int gk = 0, idx = static_cast<int>(blockIdx.x);
+      uint32_t next_ph = 0;
+      bool asked = false;   // a request is on its way
       BlockIds ids;
       Ring<kKStages> rk;
       const int withhold = withheld_tile();   // test hook: K tiles from here on are never copied
+      auto ask = [&]() {
+        if (lane == 0) {
+          // (the last answer has been read before it is written over)
+          fence_proxy_async_smem();
+          mbar_arrive_expect_tx(bar(kBarNext), 16);
+          request_block(sbase + kOffAnswer, bar(kBarNext));
+        }
+        __syncwarp();
+        asked = true;
+      };
+      // The next item's index, -1 if there is none; false: the wait ran out.
+      auto answer = [&](int& next) -> bool {
+        asked = false;
+        if (!wait(bar(kBarNext), next_ph)) return false;
+        next_ph ^= 1u;
+        next = taken_block(sbase + kOffAnswer);
+        __syncwarp();
+        return true;
+      };
+      ask();
       for (int gi = 0; ok; ++gi) {
         Item it = {};
-        for (; round < n_rounds && it.n == 0; ++round) {
-          const int idx = item_index(round);
-          if (idx < p.n_items) it = get_item(p, idx, lane);
+        while (idx >= 0) {   // items without rows are passed over
+          it = get_item(p, idx, lane);
+          if (it.n) break;
+          if (!answer(idx)) {
+            ok = false;
+            timeout = true;
+            break;
+          }
+          if (idx >= 0) ask();
         }
+        if (!ok) break;
         const int slot = gi % kRing;
         if (gi >= kRing && !wait(bar(kBarItemEmpty + slot), (gi / kRing - 1) & 1)) {
           ok = false;
@@ -348,8 +394,16 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
             __syncwarp();
           }
         }
-        if (stopped) break;
+        if (stopped || !ok) break;
+        if (!answer(idx)) {
+          ok = false;
+          timeout = true;
+        } else if (idx >= 0) {
+          ask();
+        }
       }
+      // no answer may be on its way when the block ends
+      if (asked) (void)wait(bar(kBarNext), next_ph);
     } else if (warp == kVWarp) {
       // ---------------------------------------------------------- V
       int gk = 0;
@@ -845,7 +899,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
 
 template <bool kCap, bool kBias, bool kFixed = false>
 int launch_form(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
-                const Params& prm, cudaStream_t stream) {
+                const Params& prm, unsigned blocks, cudaStream_t stream) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -856,10 +910,8 @@ int launch_form(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap&
       return PKV_ERR_LAUNCH;
     attr_set[dev] = true;
   }
-  int sms = device_sm_count();
-  if (sms <= 0) sms = 148;
-  const int grid = prm.n_items < sms ? prm.n_items : sms;
-  scored_prefill_kernel<kCap, kBias, kFixed><<<grid, kThreads, kSmemBytes, stream>>>(qm, km, vm, prm);
+  scored_prefill_kernel<kCap, kBias, kFixed>
+      <<<blocks, kThreads, kSmemBytes, stream>>>(qm, km, vm, prm);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
 
@@ -899,14 +951,14 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   prm.n_qt = (a.max_seqlen_q + kM - 1) / kM;
   const int64_t items = static_cast<int64_t>(prm.n_qt) * a.B * a.Hq;
   if (items > INT32_MAX) return PKV_ERR_SHAPE;
-  prm.n_items = static_cast<int>(items);
+  const unsigned blocks = static_cast<unsigned>(items);
   prm.num_blocks = a.num_blocks;
   prm.total_q = total_q;
   const bool cap = opt.softcap > 0.f, bias = opt.alibi_slopes != nullptr;
   if (!cap) {
     prm.scale_log2 = a.scale * 1.4426950408889634f;
-    return bias ? launch_form<false, true>(qm, km, vm, prm, stream)
-                : launch_form<false, false>(qm, km, vm, prm, stream);
+    return bias ? launch_form<false, true>(qm, km, vm, prm, blocks, stream)
+                : launch_form<false, false>(qm, km, vm, prm, blocks, stream);
   }
   prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
   prm.cap_log2 = opt.softcap * 1.4426950408889634f;
@@ -920,9 +972,9 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
     prm.poly[k] = static_cast<float>(t[k] * f);
   if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) prm.cap_x = INFINITY;
   if (!bias && prm.cap_log2 <= kFixedCap)
-    return launch_form<true, false, true>(qm, km, vm, prm, stream);
-  return bias ? launch_form<true, true>(qm, km, vm, prm, stream)
-              : launch_form<true, false>(qm, km, vm, prm, stream);
+    return launch_form<true, false, true>(qm, km, vm, prm, blocks, stream);
+  return bias ? launch_form<true, true>(qm, km, vm, prm, blocks, stream)
+              : launch_form<true, false>(qm, km, vm, prm, blocks, stream);
 }
 
 }  // namespace pkv
