@@ -69,13 +69,14 @@ constexpr int kSWarp = kQKWarp + 2;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 constexpr int kHalf = 128 * 128;           // 128 rows x 64 bf16 (one 128-byte swizzled box)
 constexpr int kTile = 2 * kHalf;           // 128 rows x 128 bf16
+constexpr int kQStages = 2;
 constexpr int kKStages = 3;
-constexpr int kVStages = 3;
+constexpr int kVStages = 2;
 constexpr int kSBufs = 3;
-static_assert(kGroups == kSBufs && kGroups == kVStages, "a group has an S buffer and V stage");
+static_assert(kGroups == kSBufs, "a group has an S buffer of its own");
 constexpr int kRing = 4;                   // item descriptors
-constexpr int kOffQ = 0;                              // one buffer
-constexpr int kOffK = kOffQ + kTile;                  // kKStages stages
+constexpr int kOffQ = 0;                              // kQStages buffers
+constexpr int kOffK = kOffQ + kQStages * kTile;       // kKStages stages
 constexpr int kOffV = kOffK + kKStages * kTile;       // kVStages stages
 constexpr int kOffM = kOffV + kVStages * kTile;       // m(t): [t & 1][row] fp32
 constexpr int kOffL = kOffM + 2 * kM * 4;             // l(t): [t & 1][row] fp32
@@ -85,9 +86,9 @@ constexpr int kOffAnswer = kOffItems + kRing * kItemBytes;
 constexpr int kOffBars = kOffAnswer + 16;
 static_assert(kOffAnswer % 16 == 0, "answer alignment");
 // barriers
-constexpr int kBarQFull = 0;
-constexpr int kBarQEmpty = 1;
-constexpr int kBarKFull = 2;                       // [K stage]
+constexpr int kBarQFull = 0;                       // [Q buffer]
+constexpr int kBarQEmpty = kBarQFull + kQStages;
+constexpr int kBarKFull = kBarQEmpty + kQStages;   // [K stage]
 constexpr int kBarKEmpty = kBarKFull + kKStages;
 constexpr int kBarVFull = kBarKEmpty + kKStages;   // [V stage]
 constexpr int kBarVEmpty = kBarVFull + kVStages;
@@ -133,6 +134,7 @@ struct Params {
   int B, Hq, Hkv, maxblk, max_q, max_k, window;
   int n_qt;          // ceil(max_q / 128)
   int64_t num_blocks, total_q;
+  bool out32;        // out is 32-byte aligned: rows are written a sector at a time
   float scale_log2;  // raw product -> log2 units; capped: -> 2 log2(e) s / c
   float cap_log2;    // the cap in log2 units
   float cap_x;       // raw product -> s / c
@@ -296,8 +298,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     bool ok = true, timeout = false;
     if (warp == kQKWarp) {
       // ---------------------------------------------------------- items, K and Q
-      // An item's Q goes into the single Q buffer right after its first K tile
-      // has been issued, once the S MMAs of the previous item are done with it.
+      // An item's Q goes into its buffer right after its first K tile has been
+      // issued, once the S MMAs of the item before the previous one are done.
       int gk = 0, idx = static_cast<int>(blockIdx.x);
       uint32_t next_ph = 0;
       bool asked = false;   // a request is on its way
@@ -377,20 +379,21 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                         bar(kBarKFull + rk.idx), (lane & 1) * 64, it.kvh, at);
           __syncwarp();
           if (kt == 0) {
-            if (gi >= 1 && !wait(bar(kBarQEmpty), (gi - 1) & 1)) {
+            const int qb = gi % kQStages;
+            if (gi >= kQStages && !wait(bar(kBarQEmpty + qb), (gi / kQStages - 1) & 1)) {
               ok = false;
               timeout = true;
               break;
             }
             if (lane == 0) {
               // rows past the sequence are its neighbour's, or zeros past total_q
-              mbar_arrive_expect_tx(bar(kBarQFull), kTile);
+              mbar_arrive_expect_tx(bar(kBarQFull + qb), kTile);
               flags[3] = gi + 1;
             }
             __syncwarp();
             if (lane >= 2 * kKStages && lane < 2 * kKStages + 2)   // lanes of their own
-              tma_load_3d(sbase + kOffQ + (lane & 1) * kHalf, &qmap, bar(kBarQFull),
-                          (lane & 1) * 64, it.h, it.row0);
+              tma_load_3d(sbase + kOffQ + qb * kTile + (lane & 1) * kHalf, &qmap,
+                          bar(kBarQFull + qb), (lane & 1) * 64, it.h, it.row0);
             __syncwarp();
           }
         }
@@ -448,8 +451,9 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         Item it;
         if (!take_item(gi, it)) { ok = false; timeout = true; break; }
         if (it.n == 0) break;
-        if (!wait(bar(kBarQFull), gi & 1)) { ok = false; timeout = true; break; }
-        const uint32_t q_s = sbase + kOffQ;
+        const int qb = gi % kQStages;
+        if (!wait(bar(kBarQFull + qb), (gi / kQStages) & 1)) { ok = false; timeout = true; break; }
+        const uint32_t q_s = sbase + kOffQ + qb * kTile;
         for (int kt = 0; kt < it.n; ++kt, ++gk, sb.next(), rk.next()) {
           if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
           // K here, and the S buffer free: the PV that read P from it (three
@@ -473,7 +477,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           umma_commit_warp(bar(kBarKEmpty + rk.idx));
         }
         if (!ok) break;
-        umma_commit_warp(bar(kBarQEmpty));
+        umma_commit_warp(bar(kBarQEmpty + qb));
       }
       // every MMA this warp issued has completed once this arrives
       umma_commit_warp(bar(kBarDrainS));
@@ -549,7 +553,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       const float inv = l > 0.f ? 1.f / l : 0.f;   // a row without keys: 0 and -inf
       const bool valid = row < e.rows;
       const int64_t at = static_cast<int64_t>(e.row0 + row) * p.Hq + e.h;
-      uint4* dst = reinterpret_cast<uint4*>(p.out + at * kHeadDim);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * kHeadDim);
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t o[32];
@@ -560,8 +564,20 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
             return pack_bf16x2(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
           };
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[4 * c + k] = make_uint4(two(8 * k), two(8 * k + 2), two(8 * k + 4), two(8 * k + 6));
+          for (int k = 0; k < 32; k += 16) {   // 16 dims: one 32-byte sector
+            uint32_t* to = dst + 16 * c + k / 2;
+            if (p.out32) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
+                           "r"(two(k)), "r"(two(k + 2)), "r"(two(k + 4)), "r"(two(k + 6)),
+                           "r"(two(k + 8)), "r"(two(k + 10)), "r"(two(k + 12)), "r"(two(k + 14))
+                           : "memory");
+            } else {
+              reinterpret_cast<uint4*>(to)[0] =
+                  make_uint4(two(k), two(k + 2), two(k + 4), two(k + 6));
+              reinterpret_cast<uint4*>(to)[1] =
+                  make_uint4(two(k + 8), two(k + 10), two(k + 12), two(k + 14));
+            }
+          }
         }
       }
       if (p.lse && valid) p.lse[at] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
@@ -569,7 +585,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     };
 
     Item prev = {};
-    uint32_t ph = 0;          // phase of the group's S buffer and V stage
+    uint32_t ph = 0;          // phase of the group's S buffer
     int gi = 0, t_item = 0;   // items, and the running count of the item's first tile
     for (; ok; ++gi) {
       Item it;
@@ -831,10 +847,11 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // keys outside [vlo, vhi]: zero their V rows so that 0 * (stale data)
         // cannot put a NaN into O (the group's thread s clears row s)
         if ((kt == 0 && tile < it.vlo) || (kt == it.n - 1 && tile + kN - 1 > it.vhi)) {
-          if (!(ok = wait(bar(kBarVFull + group), ph))) { timeout = true; break; }
+          const int vs = t % kVStages;
+          if (!(ok = wait(bar(kBarVFull + vs), (t / kVStages) & 1))) { timeout = true; break; }
           if (tile + row < it.vlo || tile + row > it.vhi) {
             const uint4 zero = make_uint4(0, 0, 0, 0);
-            const uint32_t vrow = sbase + kOffV + group * kTile + row * 128;
+            const uint32_t vrow = sbase + kOffV + vs * kTile + row * 128;
 #pragma unroll
             for (int cc = 0; cc < 8; ++cc) {
               sts128(vrow + cc * 16, zero);
@@ -883,7 +900,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     const int kin = flags[1], qin = flags[3];
     for (int x = max(0, kin - kKStages); x < kin; ++x)
       (void)slow_wait(bar(kBarKFull + x % kKStages), (x / kKStages) & 1);
-    if (qin > 0) (void)slow_wait(bar(kBarQFull), (qin - 1) & 1);
+    for (int x = max(0, qin - kQStages); x < qin; ++x)
+      (void)slow_wait(bar(kBarQFull + x % kQStages), (x / kQStages) & 1);
   }
   if (flags[0] && tid == kVWarp * 32) {
     const int vin = flags[2];
@@ -954,6 +972,7 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   const unsigned blocks = static_cast<unsigned>(items);
   prm.num_blocks = a.num_blocks;
   prm.total_q = total_q;
+  prm.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   const bool cap = opt.softcap > 0.f, bias = opt.alibi_slopes != nullptr;
   if (!cap) {
     prm.scale_log2 = a.scale * 1.4426950408889634f;
