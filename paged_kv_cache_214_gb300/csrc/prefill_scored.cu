@@ -119,7 +119,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // Caps up to this (log2 units) need no maximum: with m = 0 every weight lies in
 // 2^+-100, and sums of weights times values stay inside fp32's range.
 constexpr float kFixedCap = 100.f;
-constexpr float kTanhPoly = 0.625f;    // |s / softcap| up to which the cap is a polynomial
+constexpr float kTanhPoly = 0.45f;     // |s / softcap| up to which the cap is a polynomial
 
 struct Params {
   __nv_bfloat16* out;
@@ -138,7 +138,7 @@ struct Params {
   float scale_log2;  // raw product -> log2 units; capped: -> 2 log2(e) s / c
   float cap_log2;    // the cap in log2 units
   float cap_x;       // raw product -> s / c
-  float poly[5];     // c tanh(s / c) in log2 units = raw (poly[0] + poly[1] raw^2 + ...)
+  float poly[4];     // c tanh(s / c) in log2 units = raw (poly[0] + poly[1] raw^2 + ...)
 };
 
 // One query tile and its keys.
@@ -644,14 +644,13 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                      pack2(-2.f * slope, -2.f * slope), b);
           return b;
         };
-        // Capped: c tanh(s / c), s / c = x.  While |x| <= 0.625 in the whole warp: an
-        // odd polynomial (minimax for the absolute error, 3e-8, computed by exchange
-        // for this interval), on the FMA pipe.  Else c - 2c / (1 + e^2x), with two
+        // Capped: c tanh(s / c), s / c = x.  While |x| <= 0.45 for all products at hand
+        // of the warp: an odd polynomial (four terms, minimax for the absolute error,
+        // 5e-8, computed by exchange for this interval), on the FMA pipe.  Else c - 2c / (1 + e^2x), with two
         // special-function operations, which are scarcer.
         auto near_cap = [&](f32x2 v, f32x2 add) {
           const f32x2 u = mul2(v, v);
-          f32x2 y = fma2(pack2(p.poly[4], p.poly[4]), u, pack2(p.poly[3], p.poly[3]));
-          y = fma2(y, u, pack2(p.poly[2], p.poly[2]));
+          f32x2 y = fma2(pack2(p.poly[3], p.poly[3]), u, pack2(p.poly[2], p.poly[2]));
           y = fma2(y, u, pack2(p.poly[1], p.poly[1]));
           y = fma2(y, u, pack2(p.poly[0], p.poly[0]));
           return kFixed ? mul2(v, y) : fma2(v, y, add);
@@ -982,12 +981,12 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
   prm.cap_log2 = opt.softcap * 1.4426950408889634f;
   prm.cap_x = a.scale / opt.softcap;
-  // tanh(x) = x (t0 + t1 x^2 + ...) on |x| <= 0.625, x = raw * cap_x; the powers
+  // tanh(x) = x (t0 + t1 x^2 + ...) on |x| <= 0.45, x = raw * cap_x; the powers
   // of cap_x are folded into the coefficients, unless they would leave fp32's
   // range: every product then takes the exact form
-  const double t[5] = {0.999999459, -0.333304827, 0.132910316, -0.0513628685, 0.0145300686};
+  const double t[4] = {0.999998951, -0.333263001, 0.132051744, -0.0451495135};
   double f = static_cast<double>(prm.cap_log2) * prm.cap_x;
-  for (int k = 0; k < 5; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
+  for (int k = 0; k < 4; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
     prm.poly[k] = static_cast<float>(t[k] * f);
   if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) prm.cap_x = INFINITY;
   if (!bias && prm.cap_log2 <= kFixedCap)
