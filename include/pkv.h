@@ -490,13 +490,14 @@ int kv_cache_store_norm_rope_fp8(void* q_out, const void* q, const void* k, cons
  *   prefix_lens : int32 [B], prefill only (NULL for decode): the first
  *                 prefix_lens[b] tokens of sequence b are visible to every row,
  *                 so rows inside that prefix see it in both directions.
- * A row without keys gives out = 0 and lse = -inf.  Keys that no row of a call
- * sees are never read through a table entry that no visible key shares, and
- * their contents (infinities and NaN included) do not matter; a key that some
- * row of its sequence sees must hold finite values.
+ * A row without keys gives out = 0 and lse = -inf.  Keys below the first and
+ * above the last one that any row of their sequence sees may hold anything
+ * (infinities and NaN included), and table entries of blocks that hold none but
+ * such keys are not read (blocks freed behind a window).  Keys in between must
+ * hold finite values, in blocks of the pool.
  * All zero (or a NULL struct) is plain attention. */
 typedef struct pkv_score_options {
-  float softcap;             /* 0: none; finite, >= 0 */
+  float softcap;             /* 0: none; >= scale * 1e-30, <= 1e37 */
   int32_t window;            /* 0: none; >= 0 */
   const float* alibi_slopes;
   const int32_t* first_keys;

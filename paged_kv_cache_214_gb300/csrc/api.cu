@@ -560,6 +560,8 @@ int norm_rope_entry(NormRopeArgs a, int64_t max_positions, int D, int block_size
 int check_score_options(const pkv_score_options& o, float scale, bool decode) {
   if (!std::isfinite(scale) || scale <= 0.f) return PKV_ERR_ARG;
   if (!std::isfinite(o.softcap) || o.softcap < 0.f || o.window < 0) return PKV_ERR_ARG;
+  // scores in units of the cap, and the cap in log2 units, stay finite in fp32
+  if (o.softcap > 0.f && (o.softcap > 1e37f || scale / o.softcap > 1e30f)) return PKV_ERR_ARG;
   if (decode && o.prefix_lens) return PKV_ERR_ARG;
   if (!aligned_to(o.alibi_slopes, 4) || !aligned_to(o.first_keys, 4) ||
       !aligned_to(o.prefix_lens, 4))

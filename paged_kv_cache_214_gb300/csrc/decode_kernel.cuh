@@ -128,10 +128,19 @@ struct RowScore {
 // |dist|.  With a cap, x * qmul is 2 log2(e) s / c for the score s and the cap
 // c, and c tanh(s / c) = c - 2c / (1 + e^(2 s / c)): two special-function
 // operations, with an absolute error of a few 2^-24 of c (2^x overflows to
-// infinity, whose reciprocal is 0).
+// infinity, whose reciprocal is 0).  A cap above 100 would make that error large
+// next to small scores: those take the polynomial, whose error is relative.
+constexpr float kWideCap = 144.27f;   // 100, in log2 units
 __device__ __forceinline__ float modified_score(float x, float qmul, const RowScore& rs, int dist) {
   float v = x * qmul;
-  if (rs.cap > 0.f) v = fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(v)), rs.cap);
+  if (rs.cap > 0.f) {
+    const float x = v;
+    v = fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(x)), rs.cap);
+    if (__builtin_expect(rs.cap > kWideCap, 0)) {   // the same for the whole grid
+      const float t = x * 0.34657359f;              // s / c
+      if (fabsf(t) <= kTanhPoly) v = rs.cap * tanh_poly(t);
+    }
+  }
   return fmaf(-rs.slope, fabsf(static_cast<float>(dist)), v);
 }
 

@@ -202,6 +202,16 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
   return y;
 }
 
+// tanh(x) = x (t0 + t1 x^2 + t2 x^4 + t3 x^6) for |x| <= kTanhPoly: minimax for the
+// absolute error (5.2e-8; relative 1.05e-6), computed by exchange for the interval.
+constexpr float kTanhPoly = 0.45f;
+constexpr float kTanhT0 = 0.999998951f, kTanhT1 = -0.333263001f;
+constexpr float kTanhT2 = 0.132051744f, kTanhT3 = -0.0451495135f;
+__device__ __forceinline__ float tanh_poly(float x) {
+  const float u = x * x;
+  return x * fmaf(fmaf(fmaf(kTanhT3, u, kTanhT2), u, kTanhT1), u, kTanhT0);
+}
+
 // Two bf16 packed in a 32-bit word -> two floats (exact: bf16 is the top half
 // of a binary32).
 __device__ __forceinline__ float bf16lo(uint32_t u) { return __uint_as_float(u << 16); }

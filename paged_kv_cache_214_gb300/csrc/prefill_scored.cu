@@ -116,10 +116,9 @@ constexpr uint32_t kColO = 384;
 // precision, and moving it means waiting for the previous tile's PV.
 constexpr float kLazyRescale = 60.f;   // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
-// Caps up to this (log2 units) need no maximum: with m = 0 every weight lies in
-// 2^+-100, and sums of weights times values stay inside fp32's range.
-constexpr float kFixedCap = 100.f;
-constexpr float kTanhPoly = 0.45f;     // |s / softcap| up to which the cap is a polynomial
+// Caps up to this (log2 units; 52) need no maximum: with m = 0 every weight lies in
+// 2^+-75, and sums of 2^17 weights times values up to 2^35 in fp32's range.
+constexpr float kFixedCap = 75.f;
 
 struct Params {
   __nv_bfloat16* out;
@@ -137,7 +136,9 @@ struct Params {
   bool out32;        // out is 32-byte aligned: rows are written a sector at a time
   float scale_log2;  // raw product -> log2 units; capped: -> 2 log2(e) s / c
   float cap_log2;    // the cap in log2 units
-  float cap_x;       // raw product -> s / c
+  float cap_x;       // raw product -> s / c, infinity where only the far form is sound
+  float cap_ratio;   // raw product -> s / c
+  bool wide;         // the polynomial's coefficients leave fp32's range
   float poly[4];     // c tanh(s / c) in log2 units = raw (poly[0] + poly[1] raw^2 + ...)
 };
 
@@ -645,8 +646,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           return b;
         };
         // Capped: c tanh(s / c), s / c = x.  While |x| <= 0.45 for all products at hand
-        // of the warp: an odd polynomial (four terms, minimax for the absolute error,
-        // 5e-8, computed by exchange for this interval), on the FMA pipe.  Else c - 2c / (1 + e^2x), with two
+        // of the warp: tanh_poly on the FMA pipe, x's factor in the coefficients.  Else c - 2c / (1 + e^2x), with two
         // special-function operations, which are scarcer.
         auto near_cap = [&](f32x2 v, f32x2 add) {
           const f32x2 u = mul2(v, v);
@@ -655,11 +655,16 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           y = fma2(y, u, pack2(p.poly[0], p.poly[0]));
           return kFixed ? mul2(v, y) : fma2(v, y, add);
         };
-        auto far_cap = [&](f32x2 v, f32x2 add) {
-          v = mul2(v, sc2);
+        auto far_cap = [&](f32x2 raw, f32x2 add) {
+          f32x2 v = mul2(raw, sc2);
           v = add2(pack2(ex2(lo2(v)), ex2(hi2(v))), pack2(1.f, 1.f));
           v = fma2(pack2(rcp_approx(lo2(v)), rcp_approx(hi2(v))),
                    pack2(-2.f * p.cap_log2, -2.f * p.cap_log2), pack2(p.cap_log2, p.cap_log2));
+          if (!kFixed && p.wide) {   // (small scores: an error relative to them)
+            const float x = lo2(raw) * p.cap_ratio, y = hi2(raw) * p.cap_ratio;
+            v = pack2(fabsf(x) <= kTanhPoly ? p.cap_log2 * tanh_poly(x) : lo2(v),
+                      fabsf(y) <= kTanhPoly ? p.cap_log2 * tanh_poly(y) : hi2(v));
+          }
           return kFixed ? v : add2(v, add);
         };
         auto plain = [&](f32x2 v, f32x2 add) { return fma2(v, sc2, add); };
@@ -981,14 +986,17 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
   prm.cap_log2 = opt.softcap * 1.4426950408889634f;
   prm.cap_x = a.scale / opt.softcap;
-  // tanh(x) = x (t0 + t1 x^2 + ...) on |x| <= 0.45, x = raw * cap_x; the powers
-  // of cap_x are folded into the coefficients, unless they would leave fp32's
-  // range: every product then takes the exact form
-  const double t[4] = {0.999998951, -0.333263001, 0.132051744, -0.0451495135};
+  // tanh_poly of x = raw * cap_x: the powers of cap_x are folded into the
+  // coefficients, unless they would leave fp32's range
+  prm.cap_ratio = prm.cap_x;
+  const double t[4] = {kTanhT0, kTanhT1, kTanhT2, kTanhT3};
   double f = static_cast<double>(prm.cap_log2) * prm.cap_x;
   for (int k = 0; k < 4; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
     prm.poly[k] = static_cast<float>(t[k] * f);
-  if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) prm.cap_x = INFINITY;
+  if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) {
+    prm.cap_x = INFINITY;
+    prm.wide = true;
+  }
   if (!bias && prm.cap_log2 <= kFixedCap)
     return launch_form<true, false, true>(qm, km, vm, prm, blocks, stream);
   return bias ? launch_form<true, true>(qm, km, vm, prm, blocks, stream)

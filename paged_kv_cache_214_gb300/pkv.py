@@ -892,7 +892,9 @@ def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scale
                    stream):
     lib = _lib or load_library()
     fp8 = scales is not None
-    B = q.shape[0]
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    B = q.shape[0] if q.dim() else 0
     if not _scored_fine(q, k_cache, v_cache, block_tables, context_lens, None, B, B, B,
                         alibi_slopes, first_keys, None, out, lse,
                         torch.uint8 if fp8 else torch.bfloat16):
@@ -982,6 +984,9 @@ def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     prefix_lens[b] tokens are visible to every row of sequence b.  Returns (out
     bf16 [sum Lq, Hq, D], lse fp32 [sum Lq, Hq] or None)."""
     lib = _lib or load_library()
+    for name, t in (("q", q), ("block_tables", block_tables)):
+        if not isinstance(t, torch.Tensor) or not t.dim():
+            raise TypeError(f"{name} must be a torch.Tensor with rows")
     Nq = q.shape[0]
     B = block_tables.shape[0]
     if not _scored_fine(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, B + 1, Nq, B,

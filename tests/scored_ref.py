@@ -5,7 +5,8 @@ Bounds.  A value rounded to bf16 is off by at most 2^-8 of itself (2^-4 for
 E4M3, at least 2^-10, half its smallest step).  A score is a sum of 128 products
 in fp32: 128 roundings of at most 2^-23 of the sum of |q k| (tensor cores may
 truncate), and a handful more of the score, the cap and the bias (2^-24 each;
-the cap is exact to a few 2^-24 of itself).  A score off by d changes a key's
+the cap is exact to a few 2^-24 of itself or, above 1000, to 2^-19 of the score:
+its polynomial's relative error is 1.05e-6).  A score off by d changes a key's
 weight by the factor e^d, and so the output by at most sum_j w_j d_j (|v_j| +
 |out|) and the log-sum-exp by at most sum_j w_j d_j, to first order.  The
 prefill rounds its weights to bf16, which adds 2^-8 sum_j w_j |v_j|; the decode
@@ -56,7 +57,7 @@ def attend(q, k, v, pos, first, last, scale, softcap=0.0, slopes=None, p_step=2.
             err = 2.0 ** -23 * 136 * scale * (kh.abs() @ q[r, h].abs())
             if softcap:
                 s = softcap * torch.tanh(s / softcap)
-                err = err + 2.0 ** -21 * softcap
+                err = err + 2.0 ** -21 * min(softcap, 1000.0) + 2.0 ** -19 * s.abs()
             if slopes is not None:
                 bias = slopes[h].item() * dist
                 s = s - bias

@@ -337,8 +337,8 @@ def test_host_refusals():
 
     nan, inf = float("nan"), float("inf")
     for kw in (dict(scale=0.0), dict(scale=-1.0), dict(scale=nan), dict(scale=inf),
-               dict(softcap=-1.0), dict(softcap=nan), dict(softcap=inf), dict(window=-1),
-               dict(prefix_lens=P), dict(alibi_slopes=P + 2), dict(first_keys=P + 1), dict(B=-1),
+               dict(softcap=-1.0), dict(softcap=nan), dict(softcap=inf), dict(softcap=2e37),
+               dict(softcap=1e-33), dict(window=-1), dict(prefix_lens=P), dict(alibi_slopes=P + 2), dict(first_keys=P + 1), dict(B=-1),
                dict(Hq=0), dict(maxblk=-1), dict(splits=-1), dict(out=None), dict(q=None),
                dict(kc=None), dict(vc=None), dict(cl=None), dict(bt=None), dict(out=P + 8),
                dict(q=P), dict(q=P + 4096)):
