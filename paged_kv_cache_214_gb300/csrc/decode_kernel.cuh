@@ -124,24 +124,35 @@ struct RowScore {
   float slope;   // log2(e) * the row's distance slope
 };
 
-// Score (log2 units) of a raw product: scaled, capped, biased by the distance
-// |dist|.  With a cap, x * qmul is 2 log2(e) s / c for the score s and the cap
-// c, and c tanh(s / c) = c - 2c / (1 + e^(2 s / c)): two special-function
+// Scores (log2 units) of a lane's four raw products: scaled, capped, biased by
+// the distance.  With a cap, x * qmul is 2 log2(e) s / c for the score s and the
+// cap c, and c tanh(s / c) = c - 2c / (1 + e^(2 s / c)): two special-function
 // operations, with an absolute error of a few 2^-24 of c (2^x overflows to
 // infinity, whose reciprocal is 0).  A cap above 100 would make that error large
 // next to small scores: those take the polynomial, whose error is relative.
+// The branches are on the cap alone, the same for the whole grid: one around each
+// score cost E4M3 decode 7%.  `dist` is the distance of the first product's key,
+// the others lie 1, 8 and 9 nearer; those behind the last key are masked later.
 constexpr float kWideCap = 144.27f;   // 100, in log2 units
-__device__ __forceinline__ float modified_score(float x, float qmul, const RowScore& rs, int dist) {
-  float v = x * qmul;
+__device__ __forceinline__ void modify_scores(float (&v)[4], const RowScore& rs, int dist) {
   if (rs.cap > 0.f) {
-    const float x = v;
-    v = fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(x)), rs.cap);
-    if (__builtin_expect(rs.cap > kWideCap, 0)) {   // the same for the whole grid
-      const float t = x * 0.34657359f;              // s / c
-      if (fabsf(t) <= kTanhPoly) v = rs.cap * tanh_poly(t);
+    if (rs.cap <= kWideCap) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(v[i])), rs.cap);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float t = v[i] * 0.34657359f;   // s / c
+        v[i] = fabsf(t) <= kTanhPoly ? rs.cap * tanh_poly(t)
+                                     : fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(v[i])), rs.cap);
+      }
     }
   }
-  return fmaf(-rs.slope, fabsf(static_cast<float>(dist)), v);
+  const float d = static_cast<float>(dist);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = fmaf(-rs.slope, d - static_cast<float>(8 * (i >> 1) + (i & 1)), v[i]);
 }
 
 // Log-sum-exp merge of one output row by one warp: nsplit partials
@@ -339,13 +350,13 @@ __device__ __forceinline__ void consume_stage(uint32_t kb, uint32_t vb, int warp
   bool ok[4];
   float sv[4];
 #pragma unroll
+  for (int i = 0; i < 4; ++i) sv[i] = sc[i >> 1][i & 1] * qmul;
+  if constexpr (kScored) modify_scores(sv, rs, last - (t0 + 2 * c));
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = t0 + 8 * (i >> 1) + 2 * c + (i & 1);
     ok[i] = inside(t) && (!kMQ || t < lim);
-    if constexpr (kScored)
-      sv[i] = ok[i] ? modified_score(sc[i >> 1][i & 1], qmul, rs, last - t) : -INFINITY;
-    else
-      sv[i] = ok[i] ? sc[i >> 1][i & 1] * qmul : -INFINITY;
+    if (!ok[i]) sv[i] = -INFINITY;
   }
   float mt = fmaxf(fmaxf(sv[0], sv[1]), fmaxf(sv[2], sv[3]));
   mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));

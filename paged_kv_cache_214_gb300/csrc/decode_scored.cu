@@ -3,7 +3,7 @@
 // (pkv_score_options), on the split-K kernel of decode_kernel.cuh.
 //
 // What the options add to that kernel.  Per score: the cap, two special-function
-// operations (modified_score), and one multiply-add of the distance; both work
+// operations (modify_scores), and one multiply-add of the distance; both work
 // in log2 units.  Per block: the first key comes from the context length, so
 // with a window or documents a block's page ids are read after it (one more
 // dependent load).  Ranges start at the first key's block and the ring at its
