@@ -9,8 +9,11 @@
 // dependent load).  Ranges start at the first key's block and the ring at its
 // 64-token tile, so a window costs the bytes of the window, and pages behind it
 // are never read.  The grid covers the blocks a window can touch, not the
-// table's.  Bound by HBM as the plain decode is: a capped score's arithmetic
-// hides under the copies.
+// table's.  Bound by HBM as the plain decode is; a capped score's arithmetic hides
+// under the copies.  Measured: 64 sequences of 512 to 4096 tokens, 16 / 8 heads,
+// capped 83.9 us against 83.4 plain (524 MB, 92% of the measured copy rate); a
+// window of 1000, 32 / 8 heads, 44.5 us (259 MB, 86%); E4M3, 8 sequences of 32768
+// to 131072 tokens, 196 us (1147 MB, 86%).
 
 #include "decode_kernel.cuh"
 

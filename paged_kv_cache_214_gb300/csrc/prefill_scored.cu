@@ -10,10 +10,14 @@
 //
 // Work item: 128 rows of one sequence and query head, and the 128-key tiles from
 // the lowest lo to the highest hi of those rows, so that a window or a document
-// costs its own tiles.  Persistent: one block per SM walks the items.  16 warps:
+// costs its own tiles.  The grid has a block for every item; a block that is done
+// with its own takes over blocks that have not started (cluster launch control),
+// so that barriers and tensor memory are set up once per SM and uneven items even
+// out (two sequences of five documents, 4000 rows, 32 heads: 99 us with a fixed
+// walk over the items, 83 us so, 78 now).  16 warps:
 //   warp 12 (TMA)  finds the next item, publishes it to the other warps through
-//                  a ring of descriptors, loads its K tiles and its Q.
-//   warp 13 (TMA)  V tiles.
+//                  a ring of descriptors, loads its K tiles (3 stages) and Q (2).
+//   warp 13 (TMA)  V tiles (2 stages).
 //   warp 14 (MMA)  S_t = Q K_t^T into one of three S buffers in tensor memory.
 //   warp 15 (MMA)  O += P_t V_t, A = P_t from tensor memory, B = V_t MN-major.
 //   warps 0-11     softmax, in three groups of four: group t % 3 takes tile t of
@@ -27,8 +31,16 @@
 // on from tile t to t + 1, row by row through shared memory: the running maximum
 // m(t), as soon as the tile's maximum is known and before its 2^x, and the
 // running sum l(t), after them.  m moves only when a tile exceeds it by 2^60, so
-// that O is hardly ever rescaled.  The group that takes the first tile of the next
-// item also writes the item's output, before its P is handed to the MMA.
+// that O is hardly ever rescaled; scores capped by at most 52 need no m at all
+// (kFixed), and one pass over S instead of two.  The group that takes the first
+// tile of the next item also writes the item's output, before its P is handed to
+// the MMA.
+// Measured (b16: 16 sequences, 32 / 8 heads, 512 new rows behind 1024, 172 GFLOP):
+// capped by 50 163 us (1.05 PFLOP/s, 55% of the measured bf16 rate), by 200 182,
+// no options 155, biased 202; 8192 rows in a window of 1024 72 us.
+// Bound by the softmax warps: the tensor pipe is 49% busy, issue 50%; of a group's
+// 6100 cycles a tile, 2900 are the pass over its scores and 2000 the wait for S.
+// Handing P over in halves, so that PV starts earlier, changed nothing.
 // TMEM (512 columns): S_0 | S_1 | S_2 | O; P overlays the first 64 columns of its
 // S, in 32-key chunks behind the chunk being read.
 // Every wait is bounded: a wait that runs out records an error, the block drains
@@ -37,6 +49,7 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "pipeline.cuh"
@@ -132,6 +145,7 @@ struct Params {
   unsigned* err;
   int B, Hq, Hkv, maxblk, max_q, max_k, window;
   int n_qt;          // ceil(max_q / 128)
+  int sweep;         // sequences of a sweep (get_item)
   int64_t num_blocks, total_q;
   bool out32;        // out is 32-byte aligned: rows are written a sector at a time
   float scale_log2;  // raw product -> log2 units; capped: -> 2 log2(e) s / c
@@ -160,11 +174,15 @@ static_assert(sizeof(Item) <= kItemBytes, "descriptor");
 // Item idx, by a whole warp (the row bounds are reduced across it).
 __device__ __forceinline__ Item get_item(const Params& p, int idx, int lane) {
   Item it = {};
-  const int per_lvl = p.B * p.Hq;
-  const int lvl = idx / per_lvl;             // heavier (later) row tiles first
-  const int rem = idx - lvl * per_lvl;
-  it.b = rem / p.Hq;
-  it.h = rem - it.b * p.Hq;
+  // a sweep of sequences after another; in a sweep, heavier (later) row tiles first
+  const int per_sweep = p.sweep * p.n_qt * p.Hq;
+  const int sweep = idx / per_sweep;
+  int rem = idx - sweep * per_sweep;
+  const int per_lvl = min(p.sweep, p.B - sweep * p.sweep) * p.Hq;
+  const int lvl = rem / per_lvl;
+  rem -= lvl * per_lvl;
+  it.b = sweep * p.sweep + rem / p.Hq;
+  it.h = rem % p.Hq;
   it.kvh = it.h / (p.Hq / p.Hkv);
   const int q_begin = p.cu_q[it.b];
   const int Lq = p.cu_q[it.b + 1] - q_begin;
@@ -646,8 +664,9 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           return b;
         };
         // Capped: c tanh(s / c), s / c = x.  While |x| <= 0.45 for all products at hand
-        // of the warp: tanh_poly on the FMA pipe, x's factor in the coefficients.  Else c - 2c / (1 + e^2x), with two
-        // special-function operations, which are scarcer.
+        // of the warp: tanh_poly on the FMA pipe, x's factor in the coefficients (five
+        // terms up to 0.6 took 171 us instead of 163).  Else c - 2c / (1 + e^2x), with
+        // two special-function operations, which are scarcer.
         auto near_cap = [&](f32x2 v, f32x2 add) {
           const f32x2 u = mul2(v, v);
           f32x2 y = fma2(pack2(p.poly[3], p.poly[3]), u, pack2(p.poly[2], p.poly[2]));
@@ -888,8 +907,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     }
     if (ok && t_item > 0 && t_item % kGroups == group) {   // the last item's output
       float m = 0.f, l;
-      if (!(ok = (kFixed || receive(kBarM, m_slot, t_item - 1, m)) && receive(kBarL, l_slot, t_item - 1, l) &&
-                 epilogue(prev, gi - 1, m, l)))
+      if (!(ok = (kFixed || receive(kBarM, m_slot, t_item - 1, m)) &&
+                 receive(kBarL, l_slot, t_item - 1, l) && epilogue(prev, gi - 1, m, l)))
         timeout = true;
     }
     if (timeout && lane == 0) record_error(p.err, kErrTimeout);
@@ -974,6 +993,14 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   const int64_t items = static_cast<int64_t>(prm.n_qt) * a.B * a.Hq;
   if (items > INT32_MAX) return PKV_ERR_SHAPE;
   const unsigned blocks = static_cast<unsigned>(items);
+  // Every row tile of a sequence reads its keys again.  A sweep is as many sequences
+  // as have their K and V in a quarter of L2 (32 MB), at least one: with all 16 of
+  // b16 in one (100 MB) 177 us instead of 170 with a cold L2, 412 MB read from HBM.
+  // One sequence a sweep is as fast there, but two small ones that could mix their
+  // tiles take 78.5 us instead of 77.6.
+  const int64_t seq_bytes =
+      std::max<int64_t>(1, static_cast<int64_t>(a.max_seqlen_k) * a.Hkv * 2 * kHeadDim * 2);
+  prm.sweep = static_cast<int>(std::clamp<int64_t>((int64_t(32) << 20) / seq_bytes, 1, a.B));
   prm.num_blocks = a.num_blocks;
   prm.total_q = total_q;
   prm.out32 = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
