@@ -636,17 +636,19 @@ def _current_stream(device_index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device_index)
 
 
-def _workspace(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, handle: int):
-    """(pointer, bytes) of the caller's workspace, or of one kept for this stream
-    (calls on one stream do not overlap).  A captured call needs the caller's own: a
-    later, larger call would free the kept one under the graph."""
+def _workspace(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor,
+               handle: int) -> Optional[torch.Tensor]:
+    """The caller's workspace, or one kept for this stream (calls on one stream do not
+    overlap); hold on to it until the launch, as another thread's larger call replaces
+    the kept one.  A captured call needs the caller's own: a later, larger call would
+    free the kept one under the graph."""
     if given is not None:
         _same_device(like.device, workspace=given)
         if not given.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        return given.data_ptr(), given.numel() * given.element_size()
+        return given
     if not nbytes:
-        return 0, 0
+        return None
     if torch.cuda.is_current_stream_capturing():
         raise ValueError(f"a captured call needs a workspace of its own (zeroed, {nbytes} bytes)")
     key = (like.get_device(), handle)
@@ -654,7 +656,7 @@ def _workspace(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor, h
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(nbytes, dtype=torch.uint8, device=like.device)
         _stream_workspaces[key] = ws
-    return ws.data_ptr(), ws.numel()
+    return ws
 
 
 def _same_device(device: torch.device, **tensors):
@@ -913,7 +915,8 @@ def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scale
     num_splits = int(num_splits)
     need = _scored_workspace_bytes(at, B, Hq, Hkv, D, maxblk, bs, int(window), int(fp8),
                                    num_splits)
-    ws, ws_bytes = _workspace(workspace, need, q, handle) if need or workspace is not None else (0, 0)
+    ws = _workspace(workspace, need, q, handle) if need or workspace is not None else None
+    at_ws, ws_bytes = (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     if out is None:
         out = torch.empty_like(q)
     if lse is None and want_lse:
@@ -924,9 +927,10 @@ def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scale
     options = _score_options(softcap, alibi_slopes, window, first_keys)
     if fp8:
         status = lib.paged_decode_attention_scored_fp8(*args, float(scales[0]), float(scales[1]),
-                                                       options, ws, ws_bytes, num_splits, handle)
+                                                       options, at_ws, ws_bytes, num_splits, handle)
     else:
-        status = lib.paged_decode_attention_scored(*args, options, ws, ws_bytes, num_splits, handle)
+        status = lib.paged_decode_attention_scored(*args, options, at_ws, ws_bytes, num_splits,
+                                                   handle)
     if status != PKV_OK:
         raise PkvError(status, "paged_decode_attention_scored" + ("_fp8" if fp8 else ""))
     return out, lse
@@ -1011,8 +1015,9 @@ def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cac
         out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Nq, int(max_seqlen_q),
-        int(max_seqlen_k), Hq, Hkv, D, bs, NB, float(scale), _score_options(softcap, alibi_slopes, window, first_keys,
-                                              prefix_lens), _current_stream(at))
+        int(max_seqlen_k), Hq, Hkv, D, bs, NB, float(scale),
+        _score_options(softcap, alibi_slopes, window, first_keys, prefix_lens),
+        _current_stream(at))
     if status != PKV_OK:
         raise PkvError(status, "paged_prefill_attention_scored")
     return out, lse

@@ -120,3 +120,46 @@ def test_prefill_chunks_then_decode_steps(fp8):
             for i, s in enumerate(seqs):
                 check(s, out[i:i + 1], lse[i:i + 1], q[i:i + 1], 1, 2.0 ** -16)
     assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_past_32_bits(fp8):
+    """The same step over the first pages of a small pool and over the last pages of
+    one whose byte offsets pass 2^32 (and elements 2^31): equal results, bit for bit."""
+    hkv = 8
+    dtype, far = (torch.uint8, 16500) if fp8 else (torch.bfloat16, 8300)   # 2^18 values a page
+    g = torch.Generator().manual_seed(6)
+    T = 600
+    q, k, v = (torch.randn(T, h, D, generator=g).to(torch.bfloat16).cuda()
+               for h in (HQ, hkv, hkv))
+    place = torch.arange(T, dtype=torch.int32)
+    cos_sin = table(T, D).cuda()
+    order = torch.tensor([2, 0, 1])
+    results = []
+    for blocks in (3, far):
+        ids = (blocks - 3 + order).to(torch.int32)
+        kc, vc = (torch.empty(blocks, BS, hkv, D, dtype=dtype, device="cuda") for _ in range(2))
+        kc[-3:] = 0   # (compared whole below)
+        vc[-3:] = 0
+        slots = (ids[place.long() // BS] * BS + place % BS).cuda()
+        args = (q, k, v, kc, vc, slots, place.cuda(), cos_sin)
+        rotated = (pkv.kv_cache_store_norm_rope_fp8(*args, 0.02, 0.02) if fp8
+                   else pkv.kv_cache_store_norm_rope(*args))
+        row, lens = ids[None].cuda(), torch.tensor([T], dtype=torch.int32, device="cuda")
+        last = rotated[-1:].contiguous()
+        got = [rotated, kc[-3:].clone(), vc[-3:].clone()]
+        if fp8:
+            got += pkv.paged_decode_attention_scored_fp8(last, kc, vc, row, lens, 0.1, 0.02, 0.02,
+                                                         softcap=CAP, window=400)
+        else:
+            got += pkv.paged_decode_attention_scored(last, kc, vc, row, lens, 0.1, softcap=CAP)
+            cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+            got += pkv.paged_prefill_attention_scored(rotated, kc, vc, row, cu, cu, T, T, 0.1,
+                                                      softcap=CAP, window=400)
+        torch.cuda.synchronize()
+        results.append(got)
+        del kc, vc
+    assert int(slots.max()) * hkv * D > 2 ** 31
+    for near, distant in zip(*results):
+        assert torch.equal(near, distant)
+    assert pkv.get_device_error() == pkv.PKV_OK

@@ -237,6 +237,21 @@ def test_many_items_per_block():
 
 
 @gpu
+@pytest.mark.parametrize("max_k", [4096, 16384, 65536])
+def test_any_stated_longest_sequence(max_k):
+    """The order of the work depends on the longest sequence that the call states (all
+    five sequences together, two at a time, one at a time); the results do not."""
+    b = Batch([0, 300, 20, 0, 129], [260, 140, 1, 513, 128], 6, 2, 175)
+    tables = torch.zeros(5, max_k // 256, dtype=torch.int32)
+    tables[:, :b.tables.shape[1]] = b.tables
+    want = b.want(softcap=15.0, window=200)
+    b.max_k = max_k
+    out, lse = b.run(tables, softcap=15.0, window=200)
+    R.check(out, lse, want, f"at most {max_k}")
+    assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@gpu
 def test_rows_behind_the_last_sequence_stay():
     b = Batch([0, 40], [100, 30], 4, 2, 160)
     q = torch.cat([b.q, torch.zeros(9, 4, 128, dtype=torch.bfloat16)])
@@ -305,6 +320,23 @@ def test_captured_and_replayed():
     graph.replay()
     torch.cuda.synchronize()
     R.check(out, lse, b.want(softcap=7.0, first_keys=first.cpu()), "replay")
+    assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@gpu
+def test_two_calls_at_once():
+    """Calls of both directions on two streams; outputs made by the call itself."""
+    b = Batch([0, 700, 130], [900, 300, 513], 8, 2, 185)
+    args = [x.to("cuda") for x in (b.q, b.kc, b.vc, b.tables, b.cu_q, b.cu_k)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [pkv.paged_prefill_attention_scored(*args, b.max_q, b.max_k, b.scale, softcap=9.0,
+                                              window=300, stream=s)
+           for _ in range(20) for s in streams]
+    torch.cuda.synchronize()
+    R.check(*got[0], b.want(softcap=9.0, window=300), "two streams")
+    for out, lse in got:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
     assert pkv.get_device_error() == pkv.PKV_OK
 
 
