@@ -707,21 +707,25 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           }
         };
         if constexpr (kCap || !kBias) {
-          float big = 0.f;
-          auto chunk_big = [&](const uint32_t (&r)[32]) {
-#pragma unroll
-            for (int c = 0; c < 32; c += 2)
-              big = absmax3(big, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-          };
+          float big = 0.f, red;
           by_edge([&](auto is_edge) {
 #pragma unroll 1
             for (int c0 = 0; c0 < kN; c0 += 32) {
               const int seen = view(is_edge, c0);
               if (seen < 0) continue;
-              tmem_ld32x32_x32(s_col + c0, r0);
-              tmem_wait_ld(r0);
-              if constexpr (kCap) chunk_big(r0);
-              if constexpr (!kBias) chunk_max(r0, c0, seen);
+              if constexpr (kCap) {
+                tmem_ld32x32_x32_absmax(s_col + c0, r0, red);
+                tmem_wait_ld(r0, red);
+                big = fmaxf(big, red);
+              }
+              if constexpr (!kBias) {
+                tmem_ld32x32_x32_max(s_col + c0, r0, red);
+                tmem_wait_ld(r0, red);
+                if (is_edge && seen)
+                  chunk_max(r0, c0, seen);
+                else
+                  mx = fmaxf(mx, red);
+              }
             }
           });
           if constexpr (kCap) far = __any_sync(kFull, !(big * p.cap_x <= kTanhPoly));
@@ -837,17 +841,15 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
               tmem_st32x32_x16(s_col + c0 / 2, none);
               continue;
             }
-            tmem_ld32x32_x32(s_col + c0, r0);
-            tmem_wait_ld(r0);
             constexpr std::false_type one_way{};
             if constexpr (kFixed) {
-              float big = 0.f, big2 = 0.f;
-#pragma unroll
-              for (int c = 0; c < 32; c += 4) {
-                big = absmax3(big, __uint_as_float(r0[c]), __uint_as_float(r0[c + 1]));
-                big2 = absmax3(big2, __uint_as_float(r0[c + 2]), __uint_as_float(r0[c + 3]));
-              }
-              far = __any_sync(kFull, !(fmaxf(big, big2) * p.cap_x <= kTanhPoly));
+              float big;
+              tmem_ld32x32_x32_absmax(s_col + c0, r0, big);
+              tmem_wait_ld(r0, big);
+              far = __any_sync(kFull, !(big * p.cap_x <= kTanhPoly));
+            } else {
+              tmem_ld32x32_x32(s_col + c0, r0);
+              tmem_wait_ld(r0);
             }
             if (two_way) {
               constexpr std::integral_constant<bool, kBias> both{};
