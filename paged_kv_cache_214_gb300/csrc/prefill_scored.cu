@@ -32,9 +32,9 @@
 // m(t), as soon as the tile's maximum is known and before its 2^x, and the
 // running sum l(t), after them.  m moves only when a tile exceeds it by 2^60, so
 // that O is hardly ever rescaled; scores capped by at most 52 need no m at all
-// (kFixed), and one pass over S instead of two.  The group that takes the first
-// tile of the next item also writes the item's output, before its P is handed to
-// the MMA.
+// (kFixed), and one pass over S instead of two.  The group of an item's last tile
+// writes its output, while the others work on the next item's first tiles; that
+// item's first PV waits until O has been read.
 // Measured (b16: 16 sequences, 32 / 8 heads, 512 new rows behind 1024, 172 GFLOP):
 // capped by 50 163 us (1.05 PFLOP/s, 55% of the measured bf16 rate), by 200 182,
 // no options 155, biased 202; 8192 rows in a window of 1024 72 us.
@@ -108,8 +108,8 @@ constexpr int kBarVEmpty = kBarVFull + kVStages;
 constexpr int kBarSFull = kBarVEmpty + kVStages;   // [S buffer]
 constexpr int kBarPFull = kBarSFull + kSBufs;      // [S buffer], its group's warps
 constexpr int kBarPVDone = kBarPFull + kSBufs;     // [S buffer]: the PV that read P has completed
-constexpr int kBarOFull = kBarPVDone + kSBufs;     // the last PV of an item has completed
-constexpr int kBarDrainS = kBarOFull + 1;
+constexpr int kBarOFree = kBarPVDone + kSBufs;          // O of an item has been read, its group's warps
+constexpr int kBarDrainS = kBarOFree + 1;
 constexpr int kBarDrainPV = kBarDrainS + 1;
 constexpr int kBarItemFull = kBarDrainPV + 1;      // [descriptor]
 constexpr int kBarItemEmpty = kBarItemFull + kRing;   // [descriptor], every other warp
@@ -278,7 +278,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
-      if (i >= kBarPFull && i < kBarPFull + kSBufs) count = 4;
+      if ((i >= kBarPFull && i < kBarPFull + kSBufs) || i == kBarOFree) count = 4;
       if (i >= kBarItemEmpty && i < kBarItemEmpty + kRing) count = kSoftmaxWarps + 3;
       mbar_init(bar(i), count);
     }
@@ -514,7 +514,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         for (int kt = 0; kt < it.n; ++kt, sb.next(), rv.next()) {
           if (__any_sync(kFull, flags[0] != 0)) { ok = false; break; }
           if (!wait(bar(kBarVFull + rv.idx), rv.ph) ||
-              !wait(bar(kBarPFull + sb.idx), sb.ph)) {
+              !wait(bar(kBarPFull + sb.idx), sb.ph) ||
+              (kt == 0 && gi > 0 && !wait(bar(kBarOFree), (gi - 1) & 1))) {
             ok = false;
             timeout = true;
             break;
@@ -532,8 +533,6 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           umma_commit_warp(bar(kBarVEmpty + rv.idx));
           umma_commit_warp(bar(kBarPVDone + sb.idx));
         }
-        if (!ok) break;
-        umma_commit_warp(bar(kBarOFull));
       }
       umma_commit_warp(bar(kBarDrainPV));
       (void)wait(bar(kBarDrainPV), 0);
@@ -565,9 +564,11 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
       v = *const_cast<const volatile float*>(slot + (t & 1) * kM);
       return true;
     };
-    // Output of finished item number `done` (its m and l): O / l, row by row.
-    auto epilogue = [&](const Item& e, int done, float m, float l) -> bool {
-      if (!wait(bar(kBarOFull), done & 1)) return false;
+    // Output of an item (its m and l) by the group of its last tile, whose PV is the
+    // S buffer's phase ph: O / l, row by row.  O is then free for the
+    // next item's PV.
+    auto epilogue = [&](const Item& e, uint32_t ph, float m, float l) -> bool {
+      if (!wait(bar(kBarPVDone + group), ph)) return false;
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;   // a row without keys: 0 and -inf
       const bool valid = row < e.rows;
@@ -599,11 +600,13 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarOFree));
       if (p.lse && valid) p.lse[at] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
       return true;
     };
 
-    Item prev = {};
     uint32_t ph = 0;          // phase of the group's S buffer
     int gi = 0, t_item = 0;   // items, and the running count of the item's first tile
     for (; ok; ++gi) {
@@ -770,8 +773,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           mx *= p.scale_log2;
         }
 
-        // The running maximum.  (Received for an item's first tile as well: its
-        // slot is then free, and it is the m of the item to write.)
+        // The running maximum.  (Received for an item's first tile as well, like the
+        // sum: whoever writes t + 1 may then take the slot of t - 1.)
         if (t > 0 && !(ok = receive(kBarM, m_slot, t - 1, m_before))) { timeout = true; break; }
         const bool need = kt > 0 && mx > m_before + kLazyRescale;
         m = kt > 0 && !need ? m_before : mx;
@@ -887,31 +890,16 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         }
         tmem_wait_st();
         float l = lo2(sum2) + hi2(sum2), l_before = 0.f;
-        if (kt == 0 && t > 0) {   // this tile's PV will overwrite O: write the last item first
-          if (!(ok = receive(kBarL, l_slot, t - 1, l_before) &&
-                     epilogue(prev, gi - 1, m_before, l_before))) {
-            timeout = true;
-            break;
-          }
-        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarPFull + group));
-        if (kt > 0) {
-          if (!(ok = receive(kBarL, l_slot, t - 1, l_before))) { timeout = true; break; }
-          l = fmaf(l_before, alpha, l);
-        }
+        if (t > 0 && !(ok = receive(kBarL, l_slot, t - 1, l_before))) { timeout = true; break; }
+        if (kt > 0) l = fmaf(l_before, alpha, l);
         hand_on(kBarL, l_slot, t, l);
+        if (kt == it.n - 1 && !(ok = epilogue(it, ph, m, l))) { timeout = true; break; }
       }
       if (!ok) break;
-      prev = it;
       t_item += it.n;
-    }
-    if (ok && t_item > 0 && t_item % kGroups == group) {   // the last item's output
-      float m = 0.f, l;
-      if (!(ok = (kFixed || receive(kBarM, m_slot, t_item - 1, m)) &&
-                 receive(kBarL, l_slot, t_item - 1, l) && epilogue(prev, gi - 1, m, l)))
-        timeout = true;
     }
     if (timeout && lane == 0) record_error(p.err, kErrTimeout);
     if (!ok && lane == 0) flags[0] = 1;
