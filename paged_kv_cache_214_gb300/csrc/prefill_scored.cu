@@ -36,11 +36,13 @@
 // writes its output, while the others work on the next item's first tiles; that
 // item's first PV waits until O has been read.
 // Measured (b16: 16 sequences, 32 / 8 heads, 512 new rows behind 1024, 172 GFLOP):
-// capped by 50 163 us (1.05 PFLOP/s, 55% of the measured bf16 rate), by 200 182,
-// no options 155, biased 202; 8192 rows in a window of 1024 72 us.
-// Bound by the softmax warps: the tensor pipe is 49% busy, issue 50%; of a group's
-// 6100 cycles a tile, 2900 are the pass over its scores and 2000 the wait for S.
-// Handing P over in halves, so that PV starts earlier, changed nothing.
+// capped by 50 152 us (1.13 PFLOP/s, 59% of the measured bf16 rate), by 200 168, no
+// options 143, biased 198; 8192 rows in a window of 1024 68 us.  Bound by the chains
+// of the softmax warps: the tensor pipe is 54% busy, issue 51%.  What the last steps
+// gave: maxima reduced by the TMEM load itself 162 -> 160 (by 200: 184 -> 172), the
+// output written by the group that has just finished the item and not by the one
+// that starts the next 160 -> 152.  Without gain: P handed over in halves so that
+// PV starts earlier, O read out whole (64 packed registers) before it is written.
 // TMEM (512 columns): S_0 | S_1 | S_2 | O; P overlays the first 64 columns of its
 // S, in 32-key chunks behind the chunk being read.
 // Every wait is bounded: a wait that runs out records an error, the block drains
