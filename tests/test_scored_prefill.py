@@ -199,6 +199,18 @@ def test_maximum_that_keeps_rising(opt):
 
 
 @gpu
+@pytest.mark.parametrize("softcap", [0.0, 10.0, 200.0])
+def test_slopes_of_any_size(softcap):
+    """Slopes around 1.34, where the maximum is taken another way, steep ones, and
+    negative ones (far keys weigh more); with and without a two-way prefix."""
+    b = Batch([0, 150, 290], [200, 140, 70], 8, 2, 168)
+    slopes = torch.tensor([1.3, 1.34, 1.345, 6.0, 0.0, -1.3, -1.36, -0.01])
+    b.check("slopes", softcap=softcap, alibi_slopes=slopes)
+    b.check("slopes", softcap=softcap, alibi_slopes=slopes, window=77)
+    b.check("slopes", softcap=softcap, alibi_slopes=slopes, prefix_lens=ints([130, 40, 360]))
+
+
+@gpu
 def test_no_options_equal_plain_attention():
     b = Batch([0, 300, 17], [260, 129, 1], 8, 2, 140)
     out, lse = b.run()
