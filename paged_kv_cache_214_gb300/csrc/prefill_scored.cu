@@ -37,12 +37,13 @@
 // item's first PV waits until O has been read.
 // Measured (b16: 16 sequences, 32 / 8 heads, 512 new rows behind 1024, 172 GFLOP):
 // capped by 50 152 us (1.13 PFLOP/s, 59% of the measured bf16 rate), by 200 168, no
-// options 143, biased 198; 8192 rows in a window of 1024 68 us.  Bound by the chains
+// options 143, biased 178; 8192 rows in a window of 1024 68 us.  Bound by the chains
 // of the softmax warps: the tensor pipe is 54% busy, issue 51%.  What the last steps
 // gave: maxima reduced by the TMEM load itself 162 -> 160 (by 200: 184 -> 172), the
 // output written by the group that has just finished the item and not by the one
 // that starts the next 160 -> 152.  Without gain: P handed over in halves so that
-// PV starts earlier, O read out whole (64 packed registers) before it is written.
+// PV starts earlier, O read out whole (64 packed registers) before it is written,
+// the first pass in loads of 64 columns.
 // TMEM (512 columns): S_0 | S_1 | S_2 | O; P overlays the first 64 columns of its
 // S, in 32-key chunks behind the chunk being read.
 // Every wait is bounded: a wait that runs out records an error, the block drains
@@ -110,7 +111,7 @@ constexpr int kBarVEmpty = kBarVFull + kVStages;
 constexpr int kBarSFull = kBarVEmpty + kVStages;   // [S buffer]
 constexpr int kBarPFull = kBarSFull + kSBufs;      // [S buffer], its group's warps
 constexpr int kBarPVDone = kBarPFull + kSBufs;     // [S buffer]: the PV that read P has completed
-constexpr int kBarOFree = kBarPVDone + kSBufs;          // O of an item has been read, its group's warps
+constexpr int kBarOFree = kBarPVDone + kSBufs;     // O of an item has been read, a group's warps
 constexpr int kBarDrainS = kBarOFree + 1;
 constexpr int kBarDrainPV = kBarDrainS + 1;
 constexpr int kBarItemFull = kBarDrainPV + 1;      // [descriptor]
@@ -701,7 +702,8 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // increasing.  Biased: per 32 keys that of the products, modified as the
         // key of the greatest bias would be.  That is at most 31 slopes too high,
         // which the sums bear as they do a late maximum; steeper slopes take the
-        // maximum of the scores themselves (b16 with slopes up to 0.1: 198 us).
+        // maximum of the scores themselves (b16 with slopes up to 0.1: 178 us, with
+        // the scores' own maximum 198).
         float mx = -INFINITY;
         auto chunk_max = [&](float& mx, const uint32_t (&r)[32], int c0, int seen) {
           if (seen == 1) {
@@ -716,9 +718,9 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         };
         auto capped_max = [&](float v) {
           if constexpr (kCap)
-            return v > -INFINITY
-                       ? fmaf(-2.f * p.cap_log2, rcp_approx(1.f + ex2(v * p.scale_log2)), p.cap_log2)
-                       : v;
+            return v == -INFINITY ? v
+                                  : fmaf(-2.f * p.cap_log2,
+                                         rcp_approx(1.f + ex2(v * p.scale_log2)), p.cap_log2);
           else
             return v * p.scale_log2;
         };

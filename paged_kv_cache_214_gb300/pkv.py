@@ -996,7 +996,8 @@ def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     if not _scored_fine(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, B + 1, Nq, B,
                         alibi_slopes, first_keys, prefix_lens, out, lse, torch.bfloat16):
         _check_scored(q, k_cache, v_cache, block_tables,
-                      {"cu_seqlens_q": (cu_seqlens_q, B + 1), "cu_seqlens_k": (cu_seqlens_k, B + 1)},
+                      {"cu_seqlens_q": (cu_seqlens_q, B + 1),
+                       "cu_seqlens_k": (cu_seqlens_k, B + 1)},
                       Nq, B, alibi_slopes, first_keys, prefix_lens, out, lse, False)
     at = q.get_device()
     if stream is not None or at != _current_device():

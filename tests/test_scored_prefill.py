@@ -60,7 +60,8 @@ def test_options_and_heads(Hq, Hkv, name):
 
 
 @gpu
-@pytest.mark.parametrize("opt", [dict(softcap=20.0), dict(window=129), dict(softcap=20.0, window=128)])
+@pytest.mark.parametrize("opt", [dict(softcap=20.0), dict(window=129),
+                                 dict(softcap=20.0, window=128)])
 def test_tile_and_page_edges(opt):
     new = [127, 128, 129, 255, 256, 257]
     old = [1, 127, 128, 129, 0, 255]
@@ -402,8 +403,8 @@ def test_host_refusals():
     def prefill(out=P, q=2 * P, kc=P, vc=P, bt=P, maxblk=4, cq=P, ck=P, B=2, total=64, max_q=32,
                 max_k=500, Hq=16, Hkv=8, D=128, bs=256, NB=16, scale=0.1, **opt):
         o = pkv.ScoreOptions(**opt)
-        return lib.paged_prefill_attention_scored(out, None, q, kc, vc, bt, maxblk, cq, ck, B, total,
-                                                  max_q, max_k, Hq, Hkv, D, bs, NB, scale,
+        return lib.paged_prefill_attention_scored(out, None, q, kc, vc, bt, maxblk, cq, ck, B,
+                                                  total, max_q, max_k, Hq, Hkv, D, bs, NB, scale,
                                                   ctypes.byref(o), None)
 
     nan, inf = float("nan"), float("inf")
