@@ -573,7 +573,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     ctx = p.context_lens[b];
     const int n = ctx < 0 || ctx > cap ? cap : ctx;   // as the report below leaves it
     if (p.window > 0) lo = max(0, n - p.window);
-    if (p.first_keys) lo = max(lo, __ldg(p.first_keys + b));
+    if (p.first_keys) lo = max(lo, p.first_keys[b]);
     lo = min(lo, n);
     P = split_tokens % kBlockSize == 0 ? lo / kBlockSize * kBlockSize : lo / kTile * kTile;
   }
@@ -813,7 +813,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     RowScore rs{0.f, 0.f};
     if constexpr (kScored) {
       rs.cap = p.cap_log2;
-      if (p.slopes) rs.slope = __ldg(p.slopes + qhead(gq < G ? gq : 0)) * 1.4426950408889634f;
+      if (p.slopes) rs.slope = p.slopes[qhead(gq < G ? gq : 0)] * 1.4426950408889634f;
     }
 
     // Two groups (kGroups = 2): warps [4 grp, 4 grp + 4) take tiles grp,

@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const Params p) 
   const float* weight = which == 0 ? p.q_weight : p.k_weight;
   float4 wa = make_float4(1.f, 1.f, 1.f, 1.f), wb = wa;
   if (weight && which != 2) {
-    wa = __ldg(reinterpret_cast<const float4*>(weight + oa));
-    wb = __ldg(reinterpret_cast<const float4*>(weight + ob));
+    wa = *reinterpret_cast<const float4*>(weight + oa);
+    wb = *reinterpret_cast<const float4*>(weight + ob);
   }
   const uint16_t* const base = (which == 0 ? p.q : which == 1 ? p.k : p.v) +
                                static_cast<int64_t>(row0) * kHeadDim;
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const Params p) 
   for (int64_t t = set; t < p.T; t += sets) {
     // Everything that depends on nothing but the task is loaded first, so that
     // one latency covers the rows, the slot and the position.
-    const int64_t slot = __ldg(p.slots + t);
+    const int64_t slot = p.slots[t];
     int pos = 0;
-    if (p.R > 0) pos = __ldg(p.positions + t);
+    if (p.R > 0) pos = p.positions[t];
     const uint16_t* src = base + t * tok_stride;
     uint2 a[kRows], b[kRows];
 #pragma unroll
@@ -166,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const Params p) 
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (turns) {   // pairs 4l .. 4l + 3
       const float4* row = reinterpret_cast<const float4*>(p.cos_sin + static_cast<int64_t>(pos) * p.R);
-      c = __ldg(row + l);
-      s = __ldg(row + p.R / 8 + l);
+      c = row[l];
+      s = row[p.R / 8 + l];
     }
     // A' = A fa + B' ga, B' = B fb + A ga' as pairs of floats: own factor f, the
     // partner's factor g (weight of the partner, signed sine)
