@@ -717,12 +717,16 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           }
         };
         auto capped_max = [&](float v) {
-          if constexpr (kCap)
-            return v == -INFINITY ? v
-                                  : fmaf(-2.f * p.cap_log2,
-                                         rcp_approx(1.f + ex2(v * p.scale_log2)), p.cap_log2);
-          else
+          if constexpr (kCap) {
+            if (v == -INFINITY) return v;
+            if (p.wide) {   // (the other form may be off by more than the sums bear)
+              const float x = v * p.cap_ratio;
+              if (fabsf(x) <= kTanhPoly) return p.cap_log2 * tanh_poly(x);
+            }
+            return fmaf(-2.f * p.cap_log2, rcp_approx(1.f + ex2(v * p.scale_log2)), p.cap_log2);
+          } else {
             return v * p.scale_log2;
+          }
         };
         const bool loose = kBias && 31.f * fabsf(slope) <= kLazyRescale;
         if (kCap || !kBias || loose) {

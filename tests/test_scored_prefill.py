@@ -182,6 +182,19 @@ def test_scores_all_of_one_sign(sign, softcap):
 
 
 @gpu
+@pytest.mark.parametrize("softcap", [1e9, 1e10, 1e12, 1e30, 1e37])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_wide_caps_with_scores_of_hundreds(sign, softcap):
+    """Caps that change nothing, with every score near -200 or near 200."""
+    b = Batch([0, 130], [200, 260], 4, 2, 134)
+    b.kc.copy_(b.kc.float().abs())
+    b.q.copy_(sign * 10 * b.q.float().abs())
+    b.check("wide cap", softcap=softcap)
+    b.check("wide cap", softcap=softcap, alibi_slopes=R.alibi(4), window=100)
+    b.check("wide cap", softcap=softcap, alibi_slopes=torch.tensor([6.0, 1.4, -1.4, 0.0]))
+
+
+@gpu
 @pytest.mark.parametrize("opt", [{}, dict(softcap=300.0), dict(alibi=True), dict(window=300)])
 def test_maximum_that_keeps_rising(opt):
     """Scores that grow by hundreds from tile to tile, so that the running maximum
