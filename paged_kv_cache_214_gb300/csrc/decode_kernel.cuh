@@ -144,7 +144,7 @@ __device__ __forceinline__ void modify_scores(float (&v)[4], const RowScore& rs,
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float t = v[i] * 0.34657359f;   // s / c
-        v[i] = fabsf(t) <= kTanhPoly ? rs.cap * tanh_poly(t)
+        v[i] = fabsf(t) <= kTanhPoly ? rs.cap * (t * tanh_ratio(t))
                                      : fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(v[i])), rs.cap);
       }
     }

@@ -202,14 +202,24 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
   return y;
 }
 
-// tanh(x) = x (t0 + t1 x^2 + t2 x^4 + t3 x^6) for |x| <= kTanhPoly: minimax for the
-// absolute error (5.2e-8; relative 1.05e-6), computed by exchange for the interval.
+// tanh(x) / x = t0 + t1 x^2 + t2 x^4 + t3 x^6 for |x| <= kTanhPoly: minimax for the
+// absolute error of tanh (5.2e-8; relative 1.05e-6), computed by exchange for the
+// interval.
 constexpr float kTanhPoly = 0.45f;
 constexpr float kTanhT0 = 0.999998951f, kTanhT1 = -0.333263001f;
 constexpr float kTanhT2 = 0.132051744f, kTanhT3 = -0.0451495135f;
-__device__ __forceinline__ float tanh_poly(float x) {
+__device__ __forceinline__ float tanh_ratio(float x) {
   const float u = x * x;
-  return x * fmaf(fmaf(fmaf(kTanhT3, u, kTanhT2), u, kTanhT1), u, kTanhT0);
+  return fmaf(fmaf(fmaf(kTanhT3, u, kTanhT2), u, kTanhT1), u, kTanhT0);
+}
+
+// The cap c (log2 units) of a score s: c tanh(s / c) to a few 2^-20 of itself,
+// whatever the size of the cap (s / c may be as small as it likes; inv = 1 / c).
+__device__ __forceinline__ float cap_relative(float s, float c, float inv) {
+  const float x = s * inv;
+  return fabsf(x) <= kTanhPoly
+             ? s * tanh_ratio(x)
+             : fmaf(-2.f * c, rcp_approx(1.f + ex2(x * 2.8853900817779268f)), c);
 }
 
 // Two bf16 packed in a 32-bit word -> two floats (exact: bf16 is the top half

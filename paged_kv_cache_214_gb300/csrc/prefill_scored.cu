@@ -151,11 +151,11 @@ struct Params {
   int sweep;         // sequences of a sweep (get_item)
   int64_t num_blocks, total_q;
   bool out32;        // out is 32-byte aligned: rows are written a sector at a time
-  float scale_log2;  // raw product -> log2 units; capped: -> 2 log2(e) s / c
+  float scale_log2;  // raw product -> log2 units; capped, not wide: -> 2 log2(e) s / c
   float cap_log2;    // the cap in log2 units
-  float cap_x;       // raw product -> s / c, infinity where only the far form is sound
-  float cap_ratio;   // raw product -> s / c
-  bool wide;         // the polynomial's coefficients leave fp32's range
+  float cap_x;       // raw product -> s / c, infinity where the near form is not sound
+  float cap_inv;     // 1 / cap_log2
+  bool wide;         // capped scores by cap_relative (not kFixed)
   float poly[4];     // c tanh(s / c) in log2 units = raw (poly[0] + poly[1] raw^2 + ...)
 };
 
@@ -670,7 +670,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           return b;
         };
         // Capped: c tanh(s / c), s / c = x.  While |x| <= 0.45 for all products at hand
-        // of the warp: tanh_poly on the FMA pipe, x's factor in the coefficients (five
+        // of the warp: tanh_ratio on the FMA pipe, x's factor in the coefficients (five
         // terms up to 0.6 took 171 us instead of 163).  Else c - 2c / (1 + e^2x), with
         // two special-function operations, which are scarcer.
         auto near_cap = [&](f32x2 v, f32x2 add) {
@@ -680,16 +680,18 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           y = fma2(y, u, pack2(p.poly[0], p.poly[0]));
           return kFixed ? mul2(v, y) : fma2(v, y, add);
         };
+        // Under a wide cap that form's error, a few 2^-24 of the cap, would be large
+        // next to small scores: those take cap_relative.
         auto far_cap = [&](f32x2 raw, f32x2 add) {
           f32x2 v = mul2(raw, sc2);
+          if (!kFixed && p.wide) {
+            v = pack2(cap_relative(lo2(v), p.cap_log2, p.cap_inv),
+                      cap_relative(hi2(v), p.cap_log2, p.cap_inv));
+            return add2(v, add);
+          }
           v = add2(pack2(ex2(lo2(v)), ex2(hi2(v))), pack2(1.f, 1.f));
           v = fma2(pack2(rcp_approx(lo2(v)), rcp_approx(hi2(v))),
                    pack2(-2.f * p.cap_log2, -2.f * p.cap_log2), pack2(p.cap_log2, p.cap_log2));
-          if (!kFixed && p.wide) {   // (small scores: an error relative to them)
-            const float x = lo2(raw) * p.cap_ratio, y = hi2(raw) * p.cap_ratio;
-            v = pack2(fabsf(x) <= kTanhPoly ? p.cap_log2 * tanh_poly(x) : lo2(v),
-                      fabsf(y) <= kTanhPoly ? p.cap_log2 * tanh_poly(y) : hi2(v));
-          }
           return kFixed ? v : add2(v, add);
         };
         auto plain = [&](f32x2 v, f32x2 add) { return fma2(v, sc2, add); };
@@ -719,11 +721,10 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         auto capped_max = [&](float v) {
           if constexpr (kCap) {
             if (v == -INFINITY) return v;
-            if (p.wide) {   // (the other form may be off by more than the sums bear)
-              const float x = v * p.cap_ratio;
-              if (fabsf(x) <= kTanhPoly) return p.cap_log2 * tanh_poly(x);
-            }
-            return fmaf(-2.f * p.cap_log2, rcp_approx(1.f + ex2(v * p.scale_log2)), p.cap_log2);
+            v *= p.scale_log2;
+            // (under a wide cap the other form may be off by more than the sums bear)
+            if (p.wide) return cap_relative(v, p.cap_log2, p.cap_inv);
+            return fmaf(-2.f * p.cap_log2, rcp_approx(1.f + ex2(v)), p.cap_log2);
           } else {
             return v * p.scale_log2;
           }
@@ -1030,19 +1031,22 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
   prm.cap_log2 = opt.softcap * 1.4426950408889634f;
   prm.cap_x = a.scale / opt.softcap;
-  // tanh_poly of x = raw * cap_x: the powers of cap_x are folded into the
+  // tanh(x) / x of x = raw * cap_x: the powers of cap_x are folded into the
   // coefficients, unless they would leave fp32's range
-  prm.cap_ratio = prm.cap_x;
   const double t[4] = {kTanhT0, kTanhT1, kTanhT2, kTanhT3};
   double f = static_cast<double>(prm.cap_log2) * prm.cap_x;
   for (int k = 0; k < 4; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
     prm.poly[k] = static_cast<float>(t[k] * f);
+  const bool fixed = !bias && prm.cap_log2 <= kFixedCap;
   if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) {
     prm.cap_x = INFINITY;
-    prm.wide = true;
+    prm.wide = !fixed;
   }
-  if (!bias && prm.cap_log2 <= kFixedCap)
-    return launch_form<true, false, true>(qm, km, vm, prm, blocks, stream);
+  if (prm.wide) {
+    prm.scale_log2 = a.scale * 1.4426950408889634f;
+    prm.cap_inv = 1.f / prm.cap_log2;
+  }
+  if (fixed) return launch_form<true, false, true>(qm, km, vm, prm, blocks, stream);
   return bias ? launch_form<true, true>(qm, km, vm, prm, blocks, stream)
               : launch_form<true, false>(qm, km, vm, prm, blocks, stream);
 }

@@ -195,6 +195,18 @@ def test_wide_caps_with_scores_of_hundreds(sign, softcap):
 
 
 @gpu
+@pytest.mark.parametrize("softcap", [2e4, 1e33, 1e37])
+def test_wide_caps_with_tiny_scales(softcap):
+    """A scale of 2^-24 or so over large queries: scale / softcap may lie below the
+    smallest normal number."""
+    b = Batch([0, 130], [200, 60], 4, 2, 136)
+    b.scale *= 2.0 ** -20
+    b.q.copy_(b.q.float() * 2.0 ** 20)
+    b.check("tiny scale", softcap=softcap)
+    b.check("tiny scale", softcap=softcap, alibi_slopes=R.alibi(4))
+
+
+@gpu
 @pytest.mark.parametrize("opt", [{}, dict(softcap=300.0), dict(alibi=True), dict(window=300)])
 def test_maximum_that_keeps_rising(opt):
     """Scores that grow by hundreds from tile to tile, so that the running maximum
