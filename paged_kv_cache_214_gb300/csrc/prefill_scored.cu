@@ -1038,6 +1038,9 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   for (int k = 0; k < 4; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
     prm.poly[k] = static_cast<float>(t[k] * f);
   const bool fixed = !bias && prm.cap_log2 <= kFixedCap;
+  // (above 1000 the far form's error, a few 2^-24 of the cap, would reach 1e-4 of a
+  // score's unit, for rows that share a warp with scores past 0.45 of the cap)
+  prm.wide = !fixed && opt.softcap > 1000.f;
   if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) {
     prm.cap_x = INFINITY;
     prm.wide = !fixed;

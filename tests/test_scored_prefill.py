@@ -195,6 +195,20 @@ def test_wide_caps_with_scores_of_hundreds(sign, softcap):
 
 
 @gpu
+@pytest.mark.parametrize("opt", [{}, dict(alibi=True)])
+def test_small_scores_next_to_saturated_rows(opt):
+    """Rows whose scores are a few units, between rows (of the same warp) at the
+    ends of a wide cap."""
+    b = Batch([0, 130], [200, 260], 2, 1, 135, spread=1.0)
+    b.scale = 100.0
+    row = torch.arange(len(b.q)) % 2 == 1
+    b.q.copy_(b.q.float() * torch.where(row, 900.0, 2.7e-3)[:, None, None])
+    if opt:
+        opt = dict(alibi_slopes=R.alibi(2))
+    b.check("mixed", softcap=5e5, **opt)
+
+
+@gpu
 @pytest.mark.parametrize("softcap", [2e4, 1e33, 1e37])
 def test_wide_caps_with_tiny_scales(softcap):
     """A scale of 2^-24 or so over large queries: scale / softcap may lie below the
