@@ -108,10 +108,10 @@ struct DecodeParams {
   uint4* k_pool;                       // the pools, writable
   uint4* v_pool;
   float k_inv, v_inv;                  // E4M3 pools: binary32 1/k_scale, 1/v_scale
-  // Scored kernels: the cap in log2 units (0: none; scale_log2 then holds
-  // scale * 2 log2(e) / softcap), a distance slope per query head (null: none),
-  // the window (0: none) and the first key of each sequence's document (null:
-  // the first).
+  // Scored kernels: the cap in log2 units (0: none; up to kWideCap scale_log2
+  // then holds scale * 2 log2(e) / softcap), a distance slope per query head
+  // (null: none), the window (0: none) and the first key of each sequence's
+  // document (null: the first).
   float cap_log2;
   int window;
   const float* slopes;
@@ -125,11 +125,13 @@ struct RowScore {
 };
 
 // Scores (log2 units) of a lane's four raw products: scaled, capped, biased by
-// the distance.  With a cap, x * qmul is 2 log2(e) s / c for the score s and the
-// cap c, and c tanh(s / c) = c - 2c / (1 + e^(2 s / c)): two special-function
-// operations, with an absolute error of a few 2^-24 of c (2^x overflows to
-// infinity, whose reciprocal is 0).  A cap above 100 would make that error large
-// next to small scores: those take the polynomial, whose error is relative.
+// the distance.  With a cap up to 100, x * qmul is 2 log2(e) s / c for the score s
+// and the cap c, and c tanh(s / c) = c - 2c / (1 + e^(2 s / c)): two
+// special-function operations, with an absolute error of a few 2^-24 of c (2^x
+// overflows to infinity, whose reciprocal is 0).  A wider cap would make that error
+// large next to small scores, and x's factor in E4M3 decode (scale, k_scale and a
+// power of two over c) subnormal: there x * qmul is s itself, capped with an error
+// relative to it.
 // The branches are on the cap alone, the same for the whole grid: one around each
 // score cost E4M3 decode 7%.  `dist` is the distance of the first product's key,
 // the others lie 1, 8 and 9 nearer; those behind the last key are masked later.
@@ -141,12 +143,9 @@ __device__ __forceinline__ void modify_scores(float (&v)[4], const RowScore& rs,
       for (int i = 0; i < 4; ++i)
         v[i] = fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(v[i])), rs.cap);
     } else {
+      const float inv = rcp_approx(rs.cap);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float t = v[i] * 0.34657359f;   // s / c
-        v[i] = fabsf(t) <= kTanhPoly ? rs.cap * (t * tanh_ratio(t))
-                                     : fmaf(-2.f * rs.cap, rcp_approx(1.f + ex2(v[i])), rs.cap);
-      }
+      for (int i = 0; i < 4; ++i) v[i] = cap_relative(v[i], rs.cap, inv);
     }
   }
   const float d = static_cast<float>(dist);

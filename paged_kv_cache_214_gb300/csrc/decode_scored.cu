@@ -99,7 +99,7 @@ int launch_decode_scored(const DecodeArgs& a, const pkv_score_options& opt, cons
   DecodeParams prm = decode_params(a, plan, err);
   if (opt.softcap > 0.f) {
     prm.cap_log2 = opt.softcap * 1.4426950408889634f;
-    prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
+    if (prm.cap_log2 <= kWideCap) prm.scale_log2 = a.scale * 2.8853900817779268f / opt.softcap;
   }
   prm.window = opt.window;
   prm.slopes = opt.alibi_slopes;

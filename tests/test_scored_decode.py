@@ -174,6 +174,32 @@ def test_caps_of_any_size(softcap, fp8):
 
 @gpu
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("spread,scaled", [(20.0, 1.0), (2.0 ** -12, 2.0 ** 14), (2.0 ** 20, 2.0 ** -20)])
+@pytest.mark.parametrize("softcap", [1e12, 1e33, 1e37])
+def test_wide_caps_keep_every_bit(softcap, spread, scaled, fp8):
+    """Caps that change nothing, small and large queries: the multipliers of a raw
+    product may lie below the smallest normal number.
+
+    E4M3 pools carry a weight as two f16 numbers.  Both are multiples of 2^-24, the
+    step of f16's subnormal numbers, so the weight is off by 2^-25 at most beside
+    its relative error.  Weights are taken against a maximum that no score is below
+    in all its keys, so that their sum is at least 1: the output is off by another
+    2^-25 sum_j |v_j| over the visible keys at most."""
+    b = Batch([40, 513, 1100], 8, 2, 720, fp8, spread=spread)
+    b.scale *= scaled
+    for opt in ({}, dict(alibi_slopes=R.alibi(8), window=200)):
+        want = b.want(softcap=softcap, **opt)
+        if fp8:
+            for i, n in enumerate(b.lens.tolist()):
+                v = R.gather(b.vc, b.tables[i], n)[-opt.get("window", n):].abs() * VS
+                want[2][i] += 2.0 ** -25 * v.sum(0).repeat_interleave(4, 0)
+        out, lse = b.run(softcap=softcap, **opt)
+        R.check(out, lse, want, f"cap {softcap} {sorted(opt)}")
+    assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
 def test_no_options_equal_plain_attention(fp8):
     b = Batch([1, 300, 1000, 4100], 16, 8, 800, fp8)
     args = [x.to("cuda") for x in (b.q, b.kc, b.vc, b.tables, b.lens)]
