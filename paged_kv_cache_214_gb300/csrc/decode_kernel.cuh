@@ -474,7 +474,7 @@ __device__ __forceinline__ void store_new_row(const DecodeParams& p, int b, int 
       const __nv_bfloat16* row = is_k ? p.k_new + b * p.k_new_stride
                                       : p.v_new + b * p.v_new_stride;
       const uint4* src = reinterpret_cast<const uint4*>(row + kvh0 * kHeadDim) + 2 * (lane & 7);
-      const uint4 x0 = __ldg(src), x1 = __ldg(src + 1);
+      const uint4 x0 = src[0], x1 = src[1];
       const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
       const float inv = is_k ? p.k_inv : p.v_inv;
       uint32_t cw[4];
@@ -492,7 +492,7 @@ __device__ __forceinline__ void store_new_row(const DecodeParams& p, int b, int 
   } else {
     const __nv_bfloat16* row = lane < 16 ? p.k_new + b * p.k_new_stride
                                          : p.v_new + b * p.v_new_stride;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + kvh0 * kHeadDim) + (lane & 15));
+    const uint4 v = reinterpret_cast<const uint4*>(row + kvh0 * kHeadDim)[lane & 15];
     uint4* pool = lane < 16 ? p.k_pool : p.v_pool;
     pool[row_idx * (kHeadDim / 8) + (lane & 15)] = v;
     fence_proxy_async_global();
@@ -542,7 +542,8 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   // reads no global memory before the grids it depends on have completed
   // (with metadata_ready: none but block_tables and context_lens, which the
   // caller wrote before those grids; the wait then follows the block's
-  // early exit below, before anything else is read or written).
+  // early exit below, before anything else is read or written).  What it reads
+  // may be written while it is resident, so no load takes the read-only path.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!p.metadata_ready) asm volatile("griddepcontrol.wait;" ::: "memory");
   const int split = blockIdx.x;
@@ -581,7 +582,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
                                                           : split_tokens / kBlockSize + 2;
   int spec_id = 0;
   if (warp == 0 && lane < range_blocks && blk_begin + lane < p.maxblk)
-    spec_id = __ldg(p.block_tables + static_cast<int64_t>(b) * p.maxblk + blk_begin + lane);
+    spec_id = p.block_tables[static_cast<int64_t>(b) * p.maxblk + blk_begin + lane];
   // Context of this sequence (clamped to what its block table can address).
   if (!late) ctx = p.context_lens[b];
   if constexpr (kScored) {
@@ -615,7 +616,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
   // Fused store: the blocks of a sequence's last range write the step's new
   // token (see below); a sequence with no token to attend takes none.
   const bool store_here = !kScored && p.new_slots != nullptr && split == (nsplit > 0 ? nsplit : 1) - 1;
-  if (store_here && ctx == P && tid == 0 && __ldg(p.new_slots + b) >= 0)
+  if (store_here && ctx == P && tid == 0 && p.new_slots[b] >= 0)
     record_error(p.err, kErrIndex);
 
   if (!kScored && P > 0 && split == 0 && hg == 0 && warp == 0) {
@@ -731,7 +732,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
     // Warp 1 writes the new token's row of this kv head at its slot (see
     // store_new_row), then tells the issuing lanes, one of which waits for it
     // before copying the tile that holds the row.
-    const int sl = __ldg(p.new_slots + b);
+    const int sl = p.new_slots[b];
     if (sl >= 0) {
       const int pos = ctx - 1;
       store_new_row<kFp8>(p, b, kvh0, sl, sblk[pos / kBlockSize - blk_begin], pos, lane);
@@ -795,7 +796,7 @@ paged_decode_kernel(const __grid_constant__ CUtensorMap kmap,
             p.q + phys_row(qhead(gq)) * kHeadDim + 32 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 u = __ldg(qp + i);
+          const uint4 u = qp[i];
           qw[4 * i] = u.x;
           qw[4 * i + 1] = u.y;
           qw[4 * i + 2] = u.z;
