@@ -532,7 +532,9 @@ int paged_decode_attention_scored_fp8(void* out, float* lse, const void* q, cons
 
 /* paged_prefill_attention_scored — paged_prefill_attention under
  * pkv_score_options.  scale must be finite and > 0 and out must not overlap q.
- * q and out hold total_q rows (lse and first_keys as well).  A sequence whose
+ * q and out hold total_q rows (lse and first_keys as well); max_seqlen_q may be
+ * any bound on a sequence's rows.  A call of more than about 2^31 (128-row tile of
+ * the longest sequence, sequence, query head) items is PKV_ERR_SHAPE.  A sequence whose
  * cu_seqlens_q range leaves [0, total_q), or whose prefix_lens[b] is outside
  * [0, Lk], is reported as PKV_ERR_DEVICE_INDEX and its rows are left unwritten;
  * everything else as paged_prefill_attention. */

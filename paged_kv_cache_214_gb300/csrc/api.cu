@@ -679,6 +679,9 @@ extern "C" int paged_prefill_attention_scored(
     return PKV_ERR_ARG;
   const uint64_t bytes = 2ull * total_q * Hq * kHeadDim;
   if (overlap(out, bytes, q, bytes)) return PKV_ERR_ARG;
+  // a sequence has no more rows than all of them, whatever maximum is stated
+  if (max_seqlen_q > total_q) max_seqlen_q = static_cast<int>(total_q);
+  if (!prefill_items_fit(max_seqlen_q, B, Hq)) return PKV_ERR_SHAPE;
   unsigned* err = device_error_word();
   if (!err) return PKV_ERR_LAUNCH;
   const PrefillArgs a{out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,

@@ -180,6 +180,15 @@ struct PrefillArgs {
 };
 int launch_prefill(const PrefillArgs& a, unsigned* err, cudaStream_t stream);
 
+// Work items of a prefill call, one for each 128 rows, sequence and query head:
+// whether `rows` rows a sequence stay within 32-bit indexes (with room for a round
+// of blocks past the last item).
+inline int prefill_row_tiles(int rows) { return rows / 128 + (rows % 128 != 0); }
+inline bool prefill_items_fit(int rows, int B, int Hq) {
+  const int64_t most = INT32_MAX - (1 << 16);
+  return static_cast<int64_t>(prefill_row_tiles(rows)) * B <= most / Hq;
+}
+
 // The same under pkv_score_options; q and out hold total_q rows.
 int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score_options& opt,
                           unsigned* err, cudaStream_t stream);

@@ -1007,10 +1007,9 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   prm.max_q = a.max_seqlen_q;
   prm.max_k = a.max_seqlen_k;
   prm.window = opt.window;
-  prm.n_qt = (a.max_seqlen_q + kM - 1) / kM;
-  const int64_t items = static_cast<int64_t>(prm.n_qt) * a.B * a.Hq;
-  if (items > INT32_MAX) return PKV_ERR_SHAPE;
-  const unsigned blocks = static_cast<unsigned>(items);
+  if (!prefill_items_fit(a.max_seqlen_q, a.B, a.Hq)) return PKV_ERR_SHAPE;
+  prm.n_qt = prefill_row_tiles(a.max_seqlen_q);
+  const unsigned blocks = static_cast<unsigned>(prm.n_qt) * a.B * a.Hq;
   // Every row tile of a sequence reads its keys again.  A sweep is as many sequences
   // as have their K and V in a quarter of L2 (32 MB), at least one: with all 16 of
   // b16 in one (100 MB) 177 us instead of 170 with a cold L2, 412 MB read from HBM.

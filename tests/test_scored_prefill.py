@@ -304,6 +304,18 @@ def test_any_stated_longest_sequence(max_k):
 
 
 @gpu
+@pytest.mark.parametrize("max_q", [513, 5130, 2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 1])
+def test_any_stated_longest_chunk(max_q):
+    """A bound on the rows of a sequence, however loose, changes nothing."""
+    b = Batch([0, 300, 20], [260, 1, 513], 6, 2, 176)
+    want = b.want(softcap=15.0)
+    b.max_q = max_q
+    out, lse = b.run(softcap=15.0)
+    R.check(out, lse, want, f"at most {max_q}")
+    assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@gpu
 def test_rows_behind_the_last_sequence_stay():
     b = Batch([0, 40], [100, 30], 4, 2, 160)
     q = torch.cat([b.q, torch.zeros(9, 4, 128, dtype=torch.bfloat16)])
@@ -460,3 +472,21 @@ def test_host_refusals():
         assert prefill(**kw) == pkv.PKV_ERR_SHAPE, kw
     for kw in (dict(B=0), dict(total=0), dict(max_q=0)):
         assert prefill(q=None, **kw) == pkv.PKV_OK, kw
+
+
+def test_host_refuses_more_items_than_indexes():
+    """Items are (128-row tile, sequence, head); their number is worked out without
+    overflow and refused before anything is launched."""
+    B.build()
+    lib = pkv.load_library()
+    P, far = 1 << 24, 1 << 50
+
+    def prefill(B, total, max_q, Hq):
+        return lib.paged_prefill_attention_scored(P, None, far, P, P, P, 4, P, P, B, total, max_q,
+                                                  500, Hq, 8, 128, 256, 16, 0.1, None, None)
+
+    big = 2 ** 31 - 1
+    for max_q in (big, big - 126, big - 127):
+        assert prefill(1, big, max_q, 128) == pkv.PKV_ERR_SHAPE
+        assert prefill(2, big, max_q, 128) == pkv.PKV_ERR_SHAPE
+        assert prefill(big, big, max_q, 1024) == pkv.PKV_ERR_SHAPE
