@@ -499,6 +499,10 @@ extern "C" int paged_prefill_attention(void* out, float* lse, const void* q, con
     return PKV_ERR_ARG;
   if (static_cast<int64_t>(max_seqlen_k) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
     return PKV_ERR_ARG;
+  // the query map holds B * max_seqlen_q rows
+  if (static_cast<int64_t>(B) * max_seqlen_q > INT32_MAX ||
+      !prefill_items_fit(max_seqlen_q, B, Hq))
+    return PKV_ERR_SHAPE;
   unsigned* err = device_error_word();
   if (!err) return PKV_ERR_LAUNCH;
   PrefillArgs a{out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq, cu_seqlens_q,

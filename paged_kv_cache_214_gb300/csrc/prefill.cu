@@ -849,12 +849,11 @@ int launch_prefill(const PrefillArgs& a, unsigned* err, cudaStream_t stream) {
   prm.maxblk = a.max_blocks_per_seq;
   prm.max_q = a.max_seqlen_q;
   prm.max_k = a.max_seqlen_k;
-  prm.n_qt = (a.max_seqlen_q + kM - 1) / kM;
+  if (!prefill_items_fit(a.max_seqlen_q, a.B, a.Hq)) return PKV_ERR_SHAPE;
+  prm.n_qt = prefill_row_tiles(a.max_seqlen_q);
   prm.num_blocks = a.num_blocks;
   prm.scale_log2 = a.scale * 1.4426950408889634f;
-  const int64_t items = static_cast<int64_t>(prm.n_qt) * a.B * a.Hq;
-  if (items > INT32_MAX) return PKV_ERR_SHAPE;
-  prm.n_items = static_cast<int>(items);
+  prm.n_items = prm.n_qt * a.B * a.Hq;
   if (!set_smem_attr<kCausal>()) return PKV_ERR_LAUNCH;
   paged_prefill_kernel<kCausal><<<grid_for(prm.n_items), kThreads, kSmemBytes, stream>>>(
       qm, km, vm, prm);

@@ -196,3 +196,17 @@ def test_bindings_declare_every_signature(lib):
         for name in names:
             fn = getattr(lib, name)
             assert fn.argtypes is not None, f"{name} has no argtypes"
+
+
+def test_prefill_refuses_more_items_than_indexes(lib):
+    """(128-row tile, sequence, head) items, worked out without overflow."""
+    P, big = 1 << 24, 2 ** 31 - 1
+
+    def prefill(B, max_q, Hq):
+        return lib.paged_prefill_attention(P, None, P, P, P, P, 4, P, P, B, max_q, 500, Hq, 8, 128,
+                                           256, 16, 0.1, None)
+
+    for max_q in (big, big - 126, big - 127):
+        assert prefill(1, max_q, 128) == pkv.PKV_ERR_SHAPE
+        assert prefill(2, max_q, 8) == pkv.PKV_ERR_SHAPE
+    assert prefill(big, 1, 8) == pkv.PKV_ERR_SHAPE
