@@ -798,6 +798,14 @@ def kv_cache_store_norm_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tens
                             k_weight, eps, interleaved, q_out, stream, (k_scale, v_scale))
 
 
+def _int32(name: str, value) -> int:
+    """`value` as the library's 32-bit int (ctypes would keep its low 32 bits)."""
+    n = int(value)
+    if not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name} = {n} does not fit 32 bits")
+    return n
+
+
 @functools.lru_cache(maxsize=256)
 def _scored_workspace_bytes(device_index, B, Hq, Hkv, D, maxblk, bs, window, fp8,
                             num_splits) -> int:
@@ -810,8 +818,10 @@ def paged_decode_scored_workspace_bytes(B: int, Hq: int, Hkv: int, D: int,
                                         window: int = 0, num_splits: int = 0,
                                         fp8: bool = False) -> int:
     """Workspace of a scored decode call of these sizes on the current device."""
+    sizes = {"B": B, "Hq": Hq, "Hkv": Hkv, "D": D, "max_blocks_per_seq": max_blocks_per_seq,
+             "block_size": block_size, "window": window, "fp8": fp8, "num_splits": num_splits}
     return int(load_library().paged_decode_scored_workspace_bytes(
-        B, Hq, Hkv, D, max_blocks_per_seq, block_size, window, int(fp8), num_splits))
+        *(_int32(name, value) for name, value in sizes.items())))
 
 
 def _check_scored(q, k_cache, v_cache, block_tables, ints, rows, batch, alibi_slopes, first_keys,
@@ -883,7 +893,7 @@ def _scored_fine(q, k_cache, v_cache, block_tables, lens, lens2, n_lens, rows, b
 
 
 def _score_options(softcap, alibi_slopes, window, first_keys, prefix_lens=None) -> ScoreOptions:
-    return ScoreOptions(float(softcap), int(window),
+    return ScoreOptions(float(softcap), window,
                         None if alibi_slopes is None else alibi_slopes.data_ptr(),
                         None if first_keys is None else first_keys.data_ptr(),
                         None if prefix_lens is None else prefix_lens.data_ptr())
@@ -894,6 +904,7 @@ def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scale
                    stream):
     lib = _lib or load_library()
     fp8 = scales is not None
+    window, num_splits = _int32("window", window), _int32("num_splits", num_splits)
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     B = q.shape[0] if q.dim() else 0
@@ -912,9 +923,7 @@ def _decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scale
     NB, bs, Hkv, D = k_cache.shape
     maxblk = block_tables.shape[1]
     handle = _current_stream(at)
-    num_splits = int(num_splits)
-    need = _scored_workspace_bytes(at, B, Hq, Hkv, D, maxblk, bs, int(window), int(fp8),
-                                   num_splits)
+    need = _scored_workspace_bytes(at, B, Hq, Hkv, D, maxblk, bs, window, int(fp8), num_splits)
     ws = _workspace(workspace, need, q, handle) if need or workspace is not None else None
     at_ws, ws_bytes = (0, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     if out is None:
@@ -988,6 +997,9 @@ def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     prefix_lens[b] tokens are visible to every row of sequence b.  Returns (out
     bf16 [sum Lq, Hq, D], lse fp32 [sum Lq, Hq] or None)."""
     lib = _lib or load_library()
+    window = _int32("window", window)
+    max_seqlen_q = _int32("max_seqlen_q", max_seqlen_q)
+    max_seqlen_k = _int32("max_seqlen_k", max_seqlen_k)
     for name, t in (("q", q), ("block_tables", block_tables)):
         if not isinstance(t, torch.Tensor) or not t.dim():
             raise TypeError(f"{name} must be a torch.Tensor with rows")
@@ -1015,8 +1027,8 @@ def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     status = lib.paged_prefill_attention_scored(
         out.data_ptr(), None if lse is None else lse.data_ptr(), q.data_ptr(),
         k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Nq, int(max_seqlen_q),
-        int(max_seqlen_k), Hq, Hkv, D, bs, NB, float(scale),
+        cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Nq, max_seqlen_q,
+        max_seqlen_k, Hq, Hkv, D, bs, NB, float(scale),
         _score_options(softcap, alibi_slopes, window, first_keys, prefix_lens),
         _current_stream(at))
     if status != PKV_OK:

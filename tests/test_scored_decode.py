@@ -380,3 +380,26 @@ def test_host_refusals():
     assert lib.paged_decode_attention_scored(None, None, None, None, None, None, 1, None, 0, 16, 8,
                                              128, 256, 4, 1.0, None, None, 0, 0,
                                              None) == pkv.PKV_OK
+
+
+def test_numbers_past_32_bits_are_refused():
+    """The library takes 32-bit ints; a larger number is not cut to its low bits."""
+    B.build()
+    ten = [None] * 10   # (refused before any tensor is looked at)
+    for n in (2 ** 31, 2 ** 32, 2 ** 32 + 5, -2 ** 31 - 1):
+        for kw in (dict(window=n), dict(num_splits=n)):
+            name = next(iter(kw))
+            with pytest.raises(ValueError, match=name):
+                pkv.paged_decode_attention_scored(*ten[:6], **kw)
+            with pytest.raises(ValueError, match=name):
+                pkv.paged_decode_attention_scored_fp8(*ten[:8], **kw)
+            with pytest.raises(ValueError, match=name):
+                pkv.paged_decode_scored_workspace_bytes(4, 16, 8, 128, 16, **kw)
+        with pytest.raises(ValueError, match="max_blocks_per_seq"):
+            pkv.paged_decode_scored_workspace_bytes(4, 16, 8, 128, n)
+        with pytest.raises(ValueError, match="window"):
+            pkv.paged_prefill_attention_scored(*ten[:6], 1, 1, 1.0, window=n)
+        with pytest.raises(ValueError, match="max_seqlen_q"):
+            pkv.paged_prefill_attention_scored(*ten[:6], n, 1, 1.0)
+        with pytest.raises(ValueError, match="max_seqlen_k"):
+            pkv.paged_prefill_attention_scored(*ten[:6], 1, n, 1.0)
