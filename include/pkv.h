@@ -497,7 +497,8 @@ int kv_cache_store_norm_rope_fp8(void* q_out, const void* q, const void* k, cons
  * hold finite values, in blocks of the pool.
  * All zero (or a NULL struct) is plain attention. */
 typedef struct pkv_score_options {
-  float softcap;             /* 0: none; >= scale * 1e-30, <= 1e37 */
+  float softcap;             /* 0: none; >= scale * 1e-30 (E4M3 pools: and
+                                scale * k_scale * 1e-30), <= 1e37 */
   int32_t window;            /* 0: none; >= 0 */
   const float* alibi_slopes;
   const int32_t* first_keys;

@@ -561,11 +561,13 @@ int norm_rope_entry(NormRopeArgs a, int64_t max_positions, int D, int block_size
 }
 
 // pkv_score_options as a call may pass them.
-int check_score_options(const pkv_score_options& o, float scale, bool decode) {
+int check_score_options(const pkv_score_options& o, float scale, float k_scale, bool decode) {
   if (!std::isfinite(scale) || scale <= 0.f) return PKV_ERR_ARG;
   if (!std::isfinite(o.softcap) || o.softcap < 0.f || o.window < 0) return PKV_ERR_ARG;
   // scores in units of the cap, and the cap in log2 units, stay finite in fp32
-  if (o.softcap > 0.f && (o.softcap > 1e37f || scale / o.softcap > 1e30f)) return PKV_ERR_ARG;
+  if (o.softcap > 0.f && (o.softcap > 1e37f || scale / o.softcap > 1e30f ||
+                          scale / o.softcap * k_scale > 1e30f))
+    return PKV_ERR_ARG;
   if (decode && o.prefix_lens) return PKV_ERR_ARG;
   if (!aligned_to(o.alibi_slopes, 4) || !aligned_to(o.first_keys, 4) ||
       !aligned_to(o.prefix_lens, 4))
@@ -576,7 +578,7 @@ int check_score_options(const pkv_score_options& o, float scale, bool decode) {
 int decode_scored_entry(const DecodeArgs& a, const pkv_score_options* options, int D,
                         int block_size, pkv_stream_t stream) {
   const pkv_score_options opt = options ? *options : pkv_score_options{};
-  int st = check_score_options(opt, a.scale, true);
+  int st = check_score_options(opt, a.scale, a.fp8 ? a.k_scale : 1.f, true);
   if (st) return st;
   st = check_decode_args(a, D, block_size);
   if (st || a.B == 0) return st;
@@ -665,7 +667,7 @@ extern "C" int paged_prefill_attention_scored(
     int Hq, int Hkv, int D, int block_size, int64_t num_blocks, float scale,
     const pkv_score_options* options, pkv_stream_t stream) {
   const pkv_score_options opt = options ? *options : pkv_score_options{};
-  int st = check_score_options(opt, scale, false);
+  int st = check_score_options(opt, scale, 1.f, false);
   if (st) return st;
   if (B < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || Hq <= 0 ||
       max_blocks_per_seq < 0)

@@ -893,7 +893,10 @@ def _scored_fine(q, k_cache, v_cache, block_tables, lens, lens2, n_lens, rows, b
 
 
 def _score_options(softcap, alibi_slopes, window, first_keys, prefix_lens=None) -> ScoreOptions:
-    return ScoreOptions(float(softcap), window,
+    softcap = float(softcap)
+    if 0.0 < abs(softcap) < 1e-44:   # 32 bits would hold 0, which is no cap at all
+        raise ValueError(f"softcap = {softcap} is too small")
+    return ScoreOptions(softcap, window,
                         None if alibi_slopes is None else alibi_slopes.data_ptr(),
                         None if first_keys is None else first_keys.data_ptr(),
                         None if prefix_lens is None else prefix_lens.data_ptr())

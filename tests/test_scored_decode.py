@@ -403,3 +403,23 @@ def test_numbers_past_32_bits_are_refused():
             pkv.paged_prefill_attention_scored(*ten[:6], n, 1, 1.0)
         with pytest.raises(ValueError, match="max_seqlen_k"):
             pkv.paged_prefill_attention_scored(*ten[:6], 1, n, 1.0)
+
+
+def test_caps_too_small_for_the_arithmetic_are_refused():
+    """A cap that 32 bits round to 0 is not no cap; over E4M3 pages the multiplier of a
+    raw product, scale * k_scale / softcap, has to stay finite."""
+    B.build()
+    for softcap in (1e-50, -1e-50, 1e-45):
+        with pytest.raises(ValueError, match="softcap"):
+            pkv._score_options(softcap, None, 0, None)
+    lib, P = pkv.load_library(), 1 << 24
+
+    def decode(softcap, k_scale):
+        o = pkv.ScoreOptions(softcap=softcap)
+        return lib.paged_decode_attention_scored_fp8(P, None, 2 * P, P, P, P, 4, P, 2, 16, 8, 128,
+                                                     256, 16, 0.1, k_scale, 1.0, ctypes.byref(o),
+                                                     None, 0, 0, None)
+
+    assert decode(1e-30, 1e9) == pkv.PKV_ERR_ARG
+    assert decode(3e-23, 1e9) == pkv.PKV_ERR_ARG
+    assert decode(1e-32, 1e-9) == pkv.PKV_ERR_ARG   # (as over bf16 pages)
