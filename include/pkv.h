@@ -510,7 +510,8 @@ typedef struct pkv_score_options {
  * entries below them may be stale (blocks freed behind a window).  scale must be
  * finite and > 0, out must not overlap q, and the workspace size comes from
  * paged_decode_scored_workspace_bytes with the same arguments (fp8 != 0 for the
- * E4M3 call); everything else as paged_decode_attention. */
+ * E4M3 call).  A block table that spans about 2^31 tokens is PKV_ERR_SHAPE;
+ * everything else as paged_decode_attention. */
 size_t paged_decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D, int max_blocks_per_seq,
                                            int block_size, int window, int fp8, int num_splits);
 int paged_decode_attention_scored(void* out, float* lse, const void* q, const void* k_cache,

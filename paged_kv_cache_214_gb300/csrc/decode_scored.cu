@@ -27,6 +27,9 @@ int set_wait_hook_decode_scored(unsigned long long limit_ns, int withhold_plus1)
 int plan_decode_scored(int B, int Hq, int Hkv, int max_blocks_per_seq, int window, int num_splits,
                        int fp8, int sm_count, DecodePlan* plan) {
   if (B < 0 || window < 0 || max_blocks_per_seq < 0) return PKV_ERR_ARG;
+  // token positions are 32-bit in the kernel, those of empty ranges past the last too
+  if (max_blocks_per_seq > INT32_MAX / kBlockSize - kMaxSplits * kMaxSplitBlocks)
+    return PKV_ERR_SHAPE;
   int blocks = max_blocks_per_seq;
   const bool bounded = window > 0 && window <= static_cast<int64_t>(blocks) * kBlockSize;
   if (bounded) {

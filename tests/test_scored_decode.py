@@ -423,3 +423,20 @@ def test_caps_too_small_for_the_arithmetic_are_refused():
     assert decode(1e-30, 1e9) == pkv.PKV_ERR_ARG
     assert decode(3e-23, 1e9) == pkv.PKV_ERR_ARG
     assert decode(1e-32, 1e-9) == pkv.PKV_ERR_ARG   # (as over bf16 pages)
+
+
+def test_block_tables_of_two_to_the_31_tokens_are_refused():
+    """With a window the table may be far wider than what is read of it; positions
+    are 32-bit all the same."""
+    B.build()
+    lib, P = pkv.load_library(), 1 << 24
+
+    def decode(maxblk, window):
+        o = pkv.ScoreOptions(window=window)
+        return lib.paged_decode_attention_scored(P, None, 2 * P, P, P, P, maxblk, P, 2, 16, 8, 128,
+                                                 256, 16, 0.1, ctypes.byref(o), None, 0, 0, None)
+
+    for maxblk in (2 ** 23, 2 ** 24, 2 ** 31 - 1):
+        for window in (1, 1000, 2 ** 31 - 1):
+            assert decode(maxblk, window) == pkv.PKV_ERR_SHAPE
+    assert decode(2 ** 23 - 1, 2 ** 31 - 300) == pkv.PKV_ERR_SHAPE
