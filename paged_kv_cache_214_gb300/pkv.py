@@ -33,6 +33,7 @@ _lock = threading.Lock()
 _lib = None
 _workspaces = {}
 _stream_workspaces = {}
+_KEPT_WORKSPACES = 64   # at most; the oldest goes when another stream needs one
 
 
 class ScoreOptions(ctypes.Structure):
@@ -639,8 +640,8 @@ def _current_stream(device_index: int) -> int:
 def _workspace(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor,
                handle: int) -> Optional[torch.Tensor]:
     """The caller's workspace, or one kept for this stream (calls on one stream do not
-    overlap); hold on to it until the launch, as another thread's larger call replaces
-    the kept one.  A captured call needs the caller's own: a later, larger call would
+    overlap); hold on to it until the launch, as another thread's larger call, or one on
+    yet another stream, replaces the kept one.  A captured call needs the caller's own: a later, larger call would
     free the kept one under the graph."""
     if given is not None:
         _same_device(like.device, workspace=given)
@@ -655,7 +656,13 @@ def _workspace(given: Optional[torch.Tensor], nbytes: int, like: torch.Tensor,
     ws = _stream_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(nbytes, dtype=torch.uint8, device=like.device)
-        _stream_workspaces[key] = ws
+        with _lock:
+            # (made on its own stream, so that calls still running there are done
+            # before the allocator gives the memory to anyone else)
+            _stream_workspaces.pop(key, None)
+            while len(_stream_workspaces) >= _KEPT_WORKSPACES:
+                del _stream_workspaces[next(iter(_stream_workspaces))]
+            _stream_workspaces[key] = ws
     return ws
 
 

@@ -256,6 +256,39 @@ def test_streams_do_not_share_a_workspace():
     assert pkv.get_device_error() == pkv.PKV_OK
 
 
+def test_kept_workspaces_are_bounded(monkeypatch):
+    """A program that makes a stream for every request does not keep a workspace for
+    each of them."""
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(pkv, "_stream_workspaces", {})
+    like = torch.zeros(1)
+    for handle in range(1000):
+        ws = pkv._workspace(None, 512, like, handle)
+        assert ws.numel() >= 512 and not ws.any()
+        assert pkv._workspace(None, 256, like, handle) is ws
+        assert pkv._workspace(None, 1024, like, handle) is not ws
+    assert len(pkv._stream_workspaces) <= 64
+    assert pkv._workspace(None, 0, like, 1) is None
+
+
+@gpu
+def test_many_streams_one_after_another():
+    """More streams than workspaces are kept for, twice over."""
+    b = Batch([4000, 3000, 4096, 3500], 16, 8, 1150)
+    want = b.want(softcap=30.0)
+    args = [x.to("cuda") for x in (b.q, b.kc, b.vc, b.tables, b.lens)]
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1) for _ in range(32)]
+    streams += [torch.cuda.default_stream()]
+    torch.cuda.synchronize()
+    got = [pkv.paged_decode_attention_scored(*args, b.scale, softcap=30.0, num_splits=8, stream=s)
+           for _ in range(2) for s in streams]
+    torch.cuda.synchronize()
+    R.check(*got[0], want, "first stream")
+    for out, lse in got:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
+    assert pkv.get_device_error() == pkv.PKV_OK
+
+
 @gpu
 def test_captured_and_replayed():
     a = Batch([300, 2500, 17, 4096], 16, 8, 1200)
