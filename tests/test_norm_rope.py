@@ -231,6 +231,73 @@ def test_many_units_and_a_side_stream():
     R.check_rows(q.cpu()[pick], ref)
 
 
+def check_store(m, got, fp8, interleaved, scales=(0.02, 0.015), sample=None):
+    """Everything that a call over `m` leaves: every stored row and every slot that
+    takes none; the queries of the tokens `sample` (all of them).  Tokens whose
+    position is outside the table leave their row of q_out (7 before the call) and
+    their slot; slots past the pool, and below 0, take nothing."""
+    q, kc, vc = (x.cpu() for x in got)
+    T = len(m["slots"])
+    placed = torch.ones(T, dtype=torch.bool)
+    if m["cos_sin"] is not None:
+        placed = (m["positions"] >= 0) & (m["positions"] < m["cos_sin"].shape[0])
+    t = torch.arange(T) if sample is None else sample
+    t = t[placed[t]]
+    R.check_rows(q[t], R.norm_rope(m["q"][t], m["q_weight"], 1e-6, m["positions"][t], m["cos_sin"],
+                                   interleaved), "q")
+    assert (q[~placed] == 7.0).all()
+    stored = placed & (m["slots"] >= 0) & (m["slots"] < m["NB"] * 256)
+    at = m["slots"][stored].long()
+    kc, vc = kc.view(-1, m["Hkv"], 128), vc.view(-1, m["Hkv"], 128)
+    k = R.norm_rope(m["k"][stored], m["k_weight"], 1e-6, m["positions"][stored], m["cos_sin"],
+                    interleaved)
+    if fp8:
+        R.check_codes(kc[at], k, scales[0], "k")
+        R.check_codes(vc[at], m["v"].double()[stored], scales[1], "v")
+    else:
+        R.check_rows(kc[at], k, "k")
+        assert torch.equal(vc[at].view(torch.int16), m["v"][stored].contiguous().view(torch.int16))
+    rest = torch.ones(kc.shape[0], dtype=torch.bool)
+    rest[at] = False
+    assert not kc[rest].float().any() and not vc[rest].float().any()
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [(32, 8), (12, 4), (5, 1)])
+@pytest.mark.parametrize("rotary,interleaved,norm,odd", [
+    (128, False, True, 0), (128, True, True, 0), (64, False, True, 0), (96, True, False, 0),
+    (0, False, True, 0), (64, True, True, 1), (96, False, True, 4)])
+def test_several_rows_and_tokens_a_warp(heads, rotary, interleaved, norm, odd, fp8):
+    """Enough tokens that a half-warp takes four rows (32 / 8 heads), two (12 / 4) or
+    one (5 / 1) and goes on to a third token, with padding, slots past the pool and
+    positions outside the table in between."""
+    T = 2000
+    m = make(T, *heads, rotary=rotary, norm=norm, seed=40 + rotary, odd=odd)
+    bad = torch.arange(3, T, 41)
+    m["slots"][bad[0::4]] = -1
+    m["slots"][bad[1::4]] = m["NB"] * 256 + torch.arange(len(bad[1::4]), dtype=torch.int32)
+    m["slots"][bad[2::4]] = -2 ** 31
+    if rotary:
+        m["positions"][bad[3::4]] = 5000
+        m["positions"][bad[2::4]] = -1
+    out = torch.full((T, heads[0], 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert pkv.get_device_error() == pkv.PKV_OK
+    got = call(m, fp8=fp8, interleaved=interleaved, q_out=out)
+    assert pkv.get_device_error() == pkv.PKV_ERR_DEVICE_INDEX
+    check_store(m, got, fp8, interleaved, sample=torch.cat([bad, torch.arange(0, T, 7)]).unique())
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_every_row_of_a_large_store(fp8):
+    """Values, keys and the slots that take none, over 5000 tokens; some queries."""
+    m = make(5000, 12, 4, seed=12)
+    out = torch.full((5000, 12, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    check_store(m, call(m, fp8=fp8, q_out=out), fp8, False, sample=torch.arange(0, 5000, 37))
+    assert pkv.get_device_error() == pkv.PKV_OK
+
+
 @gpu
 def test_captured_and_replayed():
     m = make(50, 8, 2, packed=False, seed=13)
