@@ -487,14 +487,18 @@ int kv_cache_store_norm_rope_fp8(void* q_out, const void* q, const void* k, cons
  *                 first key of the row's own document; documents packed into one
  *                 sequence then do not see one another.  Any value; below 0
  *                 counts as 0, past `last` leaves the row without keys.
- *   prefix_lens : int32 [B], prefill only (NULL for decode): the first
- *                 prefix_lens[b] tokens of sequence b are visible to every row,
- *                 so rows inside that prefix see it in both directions.
+ *   prefix_lens : int32 [B], prefill only (NULL for decode): a row inside the
+ *                 first prefix_lens[b] tokens of sequence b sees up to the last of
+ *                 them, beyond its own position.  The window and first_keys bound
+ *                 the other side as ever: rows far behind the prefix see it only
+ *                 as far as those reach.
  * A row without keys gives out = 0 and lse = -inf.  Keys below the first and
  * above the last one that any row of their sequence sees may hold anything
  * (infinities and NaN included), and table entries of blocks that hold none but
  * such keys are not read (blocks freed behind a window).  Keys in between must
- * hold finite values, in blocks of the pool.
+ * hold finite values, in blocks of the pool.  The prefill call keeps its softmax
+ * weights unnormalised, within 2^+-75, until a row is complete: V's values may be
+ * as large as 2^32 (4.3e9), and contributions of values below 2^-50 may be lost.
  * All zero (or a NULL struct) is plain attention. */
 typedef struct pkv_score_options {
   float softcap;             /* 0: none; >= scale * 1e-30 (E4M3 pools: and

@@ -1003,9 +1003,10 @@ def paged_prefill_attention_scored(q: torch.Tensor, k_cache: torch.Tensor, v_cac
                                    lse: Optional[torch.Tensor] = None, want_lse: bool = True,
                                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """paged_prefill_attention with the options of paged_decode_attention_scored
-    (first_keys: int32, one per query row) and prefix_lens (int32 [B]): the first
-    prefix_lens[b] tokens are visible to every row of sequence b.  Returns (out
-    bf16 [sum Lq, Hq, D], lse fp32 [sum Lq, Hq] or None)."""
+    (first_keys: int32, one per query row) and prefix_lens (int32 [B]): rows inside
+    the first prefix_lens[b] tokens of sequence b see up to the last of them.  Values
+    may be as large as 2^32.  Returns (out bf16 [sum Lq, Hq, D], lse fp32
+    [sum Lq, Hq] or None)."""
     lib = _lib or load_library()
     window = _int32("window", window)
     max_seqlen_q = _int32("max_seqlen_q", max_seqlen_q)

@@ -239,6 +239,21 @@ def test_maximum_that_keeps_rising(opt):
 
 
 @gpu
+@pytest.mark.parametrize("size", [2.0 ** 32, 2.0 ** -40])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("softcap", [0.0, 50.0, 51.9, 300.0])
+def test_values_at_the_ends_of_their_range(softcap, sign, size):
+    """Every score at one end of the cap (or at +-86), so that weights are as large or
+    as small as they get, over values near the ends of the range that the call names."""
+    b = Batch([900, 0], [130, 300], 2, 1, 137)
+    b.kc.copy_(b.kc.float().abs())
+    b.q.copy_(sign * (60.0 if softcap else 4.0) * b.q.float().abs())
+    b.vc.copy_(size * (0.5 + torch.rand(b.vc.shape, generator=torch.Generator().manual_seed(2)) / 2))
+    b.check("values", softcap=softcap)
+    b.check("values", softcap=softcap, alibi_slopes=torch.tensor([1.3, -0.3]))
+
+
+@gpu
 @pytest.mark.parametrize("softcap", [0.0, 10.0, 200.0])
 def test_slopes_of_any_size(softcap):
     """Slopes around 1.34, where the maximum is taken another way, steep ones, and
