@@ -576,11 +576,13 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
     };
     // Output of an item (its m and l) by the group of its last tile, whose PV is the
     // S buffer's phase ph: O / l, row by row.  O is then free for the
-    // next item's PV.
-    auto epilogue = [&](const Item& e, uint32_t ph, float m, float l) -> bool {
+    // next item's PV.  A row that sees one key divides by that key's weight as P holds
+    // it, so that its output is the key's value, bit for bit.
+    auto epilogue = [&](const Item& e, uint32_t ph, float m, float l, bool one_key) -> bool {
       if (!wait(bar(kBarPVDone + group), ph)) return false;
       tc_fence_after();
-      const float inv = l > 0.f ? 1.f / l : 0.f;   // a row without keys: 0 and -inf
+      const float held = one_key ? __bfloat162float(__float2bfloat16_rn(l)) : l;
+      const float inv = l > 0.f ? 1.f / held : 0.f;   // a row without keys: 0 and -inf
       const bool valid = row < e.rows;
       const int64_t at = static_cast<int64_t>(e.row0 + row) * p.Hq + e.h;
       uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * kHeadDim);
@@ -931,7 +933,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         if (t > 0 && !(ok = receive(kBarL, l_slot, t - 1, l_before))) { timeout = true; break; }
         if (kt > 0) l = fmaf(l_before, alpha, l);
         hand_on(kBarL, l_slot, t, l);
-        if (kt == it.n - 1 && !(ok = epilogue(it, ph, m, l))) { timeout = true; break; }
+        if (kt == it.n - 1 && !(ok = epilogue(it, ph, m, l, lo == hi))) { timeout = true; break; }
       }
       if (!ok) break;
       t_item += it.n;

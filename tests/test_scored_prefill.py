@@ -239,6 +239,32 @@ def test_maximum_that_keeps_rising(opt):
 
 
 @gpu
+@pytest.mark.parametrize("softcap", [0.0, 20.0, 50.0, 300.0])
+@pytest.mark.parametrize("biased", [False, True])
+def test_rows_that_see_one_key_return_its_value(biased, softcap):
+    """A window of one token, documents of one token, the first row of a prompt: the
+    output is the value itself."""
+    b = Batch([0, 130], [200, 260], 8, 2, 138)
+    opt = dict(softcap=softcap)
+    if biased:
+        opt["alibi_slopes"] = torch.tensor([1.3, 1.34, 1.345, 6.0, 0.0, -1.3, -1.36, -0.01])
+    v = torch.cat([R.gather(b.vc, b.tables[i], o + n)[o:]
+                   for i, (o, n) in enumerate(zip(b.old, b.new))]).repeat_interleave(4, 1)
+    own = ints([o + r for o, n in zip(b.old, b.new) for r in range(n)])
+    for more in (dict(window=1), dict(first_keys=own), {}):
+        out, lse = b.run(**opt, **more)
+        R.check(out, lse, b.want(**opt, **more), f"{sorted(more)}")
+        rows = slice(None) if more else slice(0, 1)
+        assert torch.equal(out.cpu().double()[rows], v[rows])
+    # one key of a two-way prefix, behind the row itself and in another tile
+    first = torch.full((460,), 299, dtype=torch.int32)
+    out, lse = b.run(first_keys=first, prefix_lens=ints([0, 300]), **opt)
+    want = R.gather(b.vc, b.tables[1], 390)[299].repeat_interleave(4, 0)
+    assert torch.equal(out.cpu().double()[200:370], want.expand(170, 8, 128))
+    assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@gpu
 @pytest.mark.parametrize("size", [2.0 ** 32, 2.0 ** -40])
 @pytest.mark.parametrize("sign", [-1.0, 1.0])
 @pytest.mark.parametrize("softcap", [0.0, 50.0, 51.9, 300.0])
