@@ -158,11 +158,10 @@ struct Params {
   int sweep;         // sequences of a sweep (get_item)
   int64_t num_blocks, total_q;
   bool out32;        // out is 32-byte aligned: rows are written a sector at a time
-  float scale_log2;  // raw product -> log2 units; capped, not wide: -> 2 log2(e) s / c
+  float scale_log2;  // raw product -> log2 units; capped, not kWide: -> 2 log2(e) s / c
   float cap_log2;    // the cap in log2 units
   float cap_x;       // raw product -> s / c, infinity where the near form is not sound
-  float cap_inv;     // 1 / cap_log2
-  bool wide;         // capped scores by cap_relative (not kFixed)
+  float cap_inv;     // 1 / cap_log2 (kWide)
   float poly[4];     // c tanh(s / c) in log2 units = raw (poly[0] + poly[1] raw^2 + ...)
 };
 
@@ -263,8 +262,10 @@ __device__ __forceinline__ int taken_block(uint32_t answer) {
 }
 
 // kCap: capped scores; kBias: biased ones; kFixed: capped by at most kFixedCap and
-// not biased, so that m = 0 throughout and one pass over a tile's scores is enough.
-template <bool kCap, bool kBias, bool kFixed>
+// not biased, so that m = 0 throughout and one pass over a tile's scores is enough;
+// kWide: a cap so wide that the form of its far scores is cap_relative (a branch on
+// it at run time took capped and biased b16 from 231 to 266 us).
+template <bool kCap, bool kBias, bool kFixed, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1)
 scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap,
@@ -693,7 +694,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // next to small scores: those take cap_relative.
         auto far_cap = [&](f32x2 raw, f32x2 add) {
           f32x2 v = mul2(raw, sc2);
-          if (!kFixed && p.wide) {
+          if constexpr (kWide) {
             v = pack2(cap_relative(lo2(v), p.cap_log2, p.cap_inv),
                       cap_relative(hi2(v), p.cap_log2, p.cap_inv));
             return add2(v, add);
@@ -728,15 +729,14 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
           }
         };
         auto capped_max = [&](float v) {
-          if constexpr (kCap) {
-            if (v == -INFINITY) return v;
-            v *= p.scale_log2;
-            // (under a wide cap the other form may be off by more than the sums bear)
-            if (p.wide) return cap_relative(v, p.cap_log2, p.cap_inv);
-            return fmaf(-2.f * p.cap_log2, rcp_approx(1.f + ex2(v)), p.cap_log2);
-          } else {
+          if constexpr (kWide)   // (the other form may be off by more than the sums bear)
+            return v == -INFINITY ? v : cap_relative(v * p.scale_log2, p.cap_log2, p.cap_inv);
+          else if constexpr (kCap)
+            return v == -INFINITY ? v
+                                  : fmaf(-2.f * p.cap_log2,
+                                         rcp_approx(1.f + ex2(v * p.scale_log2)), p.cap_log2);
+          else
             return v * p.scale_log2;
-          }
         };
         const bool loose = kBias && 31.f * fabsf(slope) <= kLazyRescale;
         if (kCap || !kBias || loose) {
@@ -965,20 +965,20 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
   }
 }
 
-template <bool kCap, bool kBias, bool kFixed = false>
+template <bool kCap, bool kBias, bool kFixed = false, bool kWide = false>
 int launch_form(const CUtensorMap& qm, const CUtensorMap& km, const CUtensorMap& vm,
                 const Params& prm, unsigned blocks, cudaStream_t stream) {
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 64 && !attr_set[dev]) {
-    if (cudaFuncSetAttribute(scored_prefill_kernel<kCap, kBias, kFixed>,
+    if (cudaFuncSetAttribute(scored_prefill_kernel<kCap, kBias, kFixed, kWide>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemBytes) != cudaSuccess)
       return PKV_ERR_LAUNCH;
     attr_set[dev] = true;
   }
-  scored_prefill_kernel<kCap, kBias, kFixed>
+  scored_prefill_kernel<kCap, kBias, kFixed, kWide>
       <<<blocks, kThreads, kSmemBytes, stream>>>(qm, km, vm, prm);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
@@ -1045,21 +1045,22 @@ int launch_prefill_scored(const PrefillArgs& a, int64_t total_q, const pkv_score
   double f = static_cast<double>(prm.cap_log2) * prm.cap_x;
   for (int k = 0; k < 4; ++k, f *= static_cast<double>(prm.cap_x) * prm.cap_x)
     prm.poly[k] = static_cast<float>(t[k] * f);
-  const bool fixed = !bias && prm.cap_log2 <= kFixedCap;
   // (above 1000 the far form's error, a few 2^-24 of the cap, would reach 1e-4 of a
   // score's unit, for rows that share a warp with scores past 0.45 of the cap)
-  prm.wide = !fixed && opt.softcap > 1000.f;
+  bool wide = opt.softcap > 1000.f;
   if (!(prm.cap_x > 1e-4f && prm.cap_x < 1e3f && f > 1e-36 && f < 1e36)) {
     prm.cap_x = INFINITY;
-    prm.wide = !fixed;
+    wide = true;
   }
-  if (prm.wide) {
-    prm.scale_log2 = a.scale * 1.4426950408889634f;
-    prm.cap_inv = 1.f / prm.cap_log2;
-  }
-  if (fixed) return launch_form<true, false, true>(qm, km, vm, prm, blocks, stream);
-  return bias ? launch_form<true, true>(qm, km, vm, prm, blocks, stream)
-              : launch_form<true, false>(qm, km, vm, prm, blocks, stream);
+  if (!bias && prm.cap_log2 <= kFixedCap)   // (an error of 2^-24 of such a cap is no matter)
+    return launch_form<true, false, true>(qm, km, vm, prm, blocks, stream);
+  if (!wide)
+    return bias ? launch_form<true, true>(qm, km, vm, prm, blocks, stream)
+                : launch_form<true, false>(qm, km, vm, prm, blocks, stream);
+  prm.scale_log2 = a.scale * 1.4426950408889634f;
+  prm.cap_inv = 1.f / prm.cap_log2;
+  return bias ? launch_form<true, true, false, true>(qm, km, vm, prm, blocks, stream)
+              : launch_form<true, false, false, true>(qm, km, vm, prm, blocks, stream);
 }
 
 }  // namespace pkv
