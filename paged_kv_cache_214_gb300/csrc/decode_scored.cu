@@ -10,10 +10,11 @@
 // 64-token tile, so a window costs the bytes of the window, and pages behind it
 // are never read.  The grid covers the blocks a window can touch, not the
 // table's.  Bound by HBM as the plain decode is; a capped score's arithmetic hides
-// under the copies.  Measured: 64 sequences of 512 to 4096 tokens, 16 / 8 heads,
-// capped 83.9 us against 83.4 plain (524 MB, 92% of the measured copy rate); a
-// window of 1000, 32 / 8 heads, 44.5 us (259 MB, 86%); E4M3, 8 sequences of 32768
-// to 131072 tokens, 196 us (1147 MB, 86%).
+// under the copies.  Measured on 64 sequences of 512 to 4096 tokens, 16 / 8 heads: a
+// batch of 524 MB capped 84.9 us against 84.4 plain (91% of the measured copy rate),
+// one of 594 MB capped 96.4 (91%).  A window of 1000, 64 sequences, 32 / 8 heads: 45
+// us (259 MB, 85%).  E4M3, 8 sequences of 32768 to 131072 tokens, capped: 198 us
+// (1147 MB, 85%).
 
 #include "decode_kernel.cuh"
 

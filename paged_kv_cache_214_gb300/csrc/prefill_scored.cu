@@ -35,15 +35,17 @@
 // (kFixed), and one pass over S instead of two.  The group of an item's last tile
 // writes its output, while the others work on the next item's first tiles; that
 // item's first PV waits until O has been read.
-// Measured (b16: 16 sequences, 32 / 8 heads, 512 new rows behind 1024, 172 GFLOP):
-// capped by 50 152 us (1.13 PFLOP/s, 59% of the measured bf16 rate), by 200 168, no
-// options 143, biased 178; 8192 rows in a window of 1024 68 us.  Bound by the chains
-// of the softmax warps: the tensor pipe is 54% busy, issue 51%.  What the last steps
-// gave: maxima reduced by the TMEM load itself 162 -> 160 (by 200: 184 -> 172), the
-// output written by the group that has just finished the item and not by the one
-// that starts the next 160 -> 152.  Without gain: P handed over in halves so that
-// PV starts earlier, O read out whole (64 packed registers) before it is written,
-// the first pass in loads of 64 columns.
+// Measured (b16: 16 sequences, 32 / 8 heads, 512 new rows behind 1024, 172 GFLOP;
+// the kernel, warm L2): capped by 50 150 us (1.15 PFLOP/s, 60% of the measured bf16
+// rate), by 200 165, no options 140, biased 177; 8192 rows in a window of 1024 66 us.
+// With inputs that are not in L2 capped by 50 takes 160 us (56%), the window 68.
+// Bound by the chains of the softmax warps: the tensor pipe is 54% busy, issue 51%.
+// What the last steps gave: maxima reduced by the TMEM load itself 162 -> 160 (by
+// 200: 184 -> 172), the output written by the group that has just finished the item
+// and not by the one that starts the next 160 -> 152.  Caps past 1000 keep an error
+// relative to the score (cap_relative) and take 312.  Without gain: P handed over in
+// halves so that PV starts earlier, O read out whole (64 packed registers) before it
+// is written, the first pass in loads of 64 columns.
 // TMEM (512 columns): S_0 | S_1 | S_2 | O; P overlays the first 64 columns of its
 // S, in 32-key chunks behind the chunk being read.
 // Rounding: P goes to the second product as bf16, as both operands of a tcgen05
@@ -139,7 +141,7 @@ constexpr float kLazyRescale = 60.f;   // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
 // Caps up to this (log2 units; 52) need no maximum: with m = 0 every weight lies in
 // 2^+-75, and sums of 2^20 weights times values up to 2^32 in fp32's range (the
-// range that the call documents; a maximum for these rows too would cost 12%, the
+// range that the call documents; a maximum for these rows too would cost 10%, the
 // difference of caps 50 and 200 above).
 constexpr float kFixedCap = 75.f;
 
@@ -714,7 +716,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap qmap,
         // increasing.  Biased: per 32 keys that of the products, modified as the
         // key of the greatest bias would be.  That is at most 31 slopes too high,
         // which the sums bear as they do a late maximum; steeper slopes take the
-        // maximum of the scores themselves (b16 with slopes up to 0.1: 178 us, with
+        // maximum of the scores themselves (b16 with slopes up to 0.1: 177 us, with
         // the scores' own maximum 198).
         float mx = -INFINITY;
         auto chunk_max = [&](float& mx, const uint32_t (&r)[32], int c0, int seen) {
