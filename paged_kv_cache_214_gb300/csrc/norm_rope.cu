@@ -29,7 +29,7 @@
 // MB): 60 us with rows of contiguous dims, partners exchanged by shuffles and all
 // three tensors in one warp (93 instructions a row), 45 us in this layout with one
 // task a warp and each row reduced by itself, 38 us now (5.4 TB/s, 80% of the
-// measured copy; 36.9 in the kernel alone).  Loading the next token's rows ahead
+// measured copy; 36 to 37 in the kernel alone).  Loading the next token's rows ahead
 // (more registers) took 42.  Into E4M3 pages (189 MB) 38 us too.
 
 #include <cuda_bf16.h>
