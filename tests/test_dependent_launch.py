@@ -74,3 +74,77 @@ def test_steps_without_a_pause_equal_steps_one_by_one(call, fp8):
     for (a, la), (b, lb) in zip(run(lambda: None), run(torch.cuda.synchronize)):
         assert torch.equal(a, b) and torch.equal(la, lb)
     assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [False, True])
+def test_captured_steps_equal_steps_one_by_one(fp8):
+    """Four steps of store and decode in one graph, over buffers that change between
+    replays."""
+    B, Hq, Hkv, D, steps = 24, 16, 8, 128, 4
+    g = torch.Generator(device="cuda").manual_seed(4)
+    table = torch.randperm(2 * B, generator=g, device="cuda").to(torch.int32).view(B, 2)
+    angle = torch.rand(512, 64, generator=g, device="cuda") * 6.28
+    cos_sin = torch.cat([angle.cos(), angle.sin()], 1)
+    rows = torch.empty(steps, B, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device="cuda")
+    first = torch.empty(B, dtype=torch.int32, device="cuda")
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    kc = torch.zeros(2 * B, 256, Hkv, D, dtype=dtype, device="cuda")
+    vc = torch.zeros_like(kc)
+    q = torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda")
+    outs = [torch.empty(B, Hq, D, dtype=torch.bfloat16, device="cuda") for _ in range(steps)]
+    lses = [torch.empty(B, Hq, device="cuda") for _ in range(steps)]
+    need = pkv.paged_decode_scored_workspace_bytes(B, Hq, Hkv, D, 2, fp8=fp8, num_splits=2)
+    ws = torch.zeros(max(need, 256), dtype=torch.uint8, device="cuda")
+
+    def run(pause=lambda: None):
+        for t in range(steps):
+            places = first + t
+            page = (places // 256).long()
+            slots = table.gather(1, page[:, None])[:, 0] * 256 + places % 256
+            lens = places + 1
+            pause()
+            args = (rows[t, :, :Hq], rows[t, :, Hq:Hq + Hkv], rows[t, :, Hq + Hkv:], kc, vc, slots,
+                    places, cos_sin)
+            if fp8:
+                pkv.kv_cache_store_norm_rope_fp8(*args, 0.02, 0.02, q_out=q)
+            else:
+                pkv.kv_cache_store_norm_rope(*args, q_out=q)
+            pause()
+            more = dict(softcap=20.0, out=outs[t], lse=lses[t], workspace=ws, num_splits=2)
+            if fp8:
+                pkv.paged_decode_attention_scored_fp8(q, kc, vc, table, lens, 0.1, 0.02, 0.02, **more)
+            else:
+                pkv.paged_decode_attention_scored(q, kc, vc, table, lens, 0.1, **more)
+            pause()
+
+    def fill(seed):
+        h = torch.Generator(device="cuda").manual_seed(seed)
+        rows.copy_(torch.randn(rows.shape, generator=h, device="cuda"))
+        first.copy_(torch.randint(200, 500, (B,), generator=h, device="cuda"))
+        pool = torch.randn(kc.shape, generator=h, device="cuda")
+        kc.copy_((pool * 40).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8) if fp8
+                 else pool)
+        vc.copy_(kc.flip(0))
+
+    fill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    for seed in (1, 2, 3):
+        fill(seed)
+        run(torch.cuda.synchronize)
+        want = [x.clone() for x in (*outs, *lses, kc, vc)]
+        fill(seed)
+        for x in (*outs, *lses):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*outs, *lses, kc, vc), want):
+            assert torch.equal(a, b)
+    assert pkv.get_device_error() == pkv.PKV_OK
