@@ -565,8 +565,9 @@ extern "C" int paged_append_tokens(int32_t* slot_mapping, int32_t* positions,
                        static_cast<int>(num_blocks), static_cast<unsigned*>(workspace), err};
   auto smem_of = [](size_t rows) { return (3 * rows + 2) * sizeof(int); };
   const size_t smem = smem_of(R);
-  // (always to the most that a call can need: another thread may be about to launch)
-  if (smem > 48 * 1024 &&
+  // Without the attribute 48 KB hold the kernel's static shared memory (half a KB) too.  (Always
+  // to the most that a call can need: another thread may be about to launch.)
+  if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(append_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem_of(kMaxRows))) != cudaSuccess)
     return PKV_ERR_LAUNCH;
