@@ -174,10 +174,15 @@ __device__ __forceinline__ float sum16(const float (&x)[16], float m) {
   return s;
 }
 
-// Factor that takes a sum against m to one against the larger maximum n.
+// Factor that takes a sum against m to one against the larger maximum n.  Each is kept as its own
+// maximum says: with one beyond kFar and one not, the near one's C is taken as it is and the far
+// one's logarithm worked out to its difference from C (its rounding alone would leave 2^-11).
 __device__ __forceinline__ float shift(float m, float n) {
   if (m == -INFINITY) return 0.f;
-  if (fabsf(m) <= kFar && fabsf(n) <= kFar) return ex2(reference(m) - reference(n));
+  const bool near_m = fabsf(m) <= kFar, near_n = fabsf(n) <= kFar;
+  if (near_m && near_n) return ex2(reference(m) - reference(n));
+  if (near_m) return ex2(fmaf(-n, kLog2eLo, fmaf(-n, kLog2eHi, reference(m))));
+  if (near_n) return ex2(fmaf(m, kLog2eLo, fmaf(m, kLog2eHi, -reference(n))));
   return m == n ? 1.f : ex2((m - n) * kLog2eHi);
 }
 
