@@ -623,8 +623,8 @@ int paged_append_tokens(int32_t* slot_mapping, int32_t* positions, int32_t* cu_s
  *     among them); their out_end is -inf.
  * logits : bf16 (logits_fp32 == 0) or fp32, row (b, w) at logits + (b * width + w) *
  *   row_stride elements, aligned to its element.  V >= 1, row_stride >= V.
- * scores : fp32 [B, width].  1 <= width <= 32, 1 <= num_out <= 64, width * V < 2^31
- *   (else PKV_ERR_SHAPE).
+ * scores : fp32 [B, width].  1 <= width <= 32, 1 <= num_out <= 64, width * V < 2^31 - 1024,
+ *   B * width <= 65535 (else PKV_ERR_SHAPE).
  * Returns PKV_OK, PKV_ERR_ARG, PKV_ERR_SHAPE, PKV_ERR_WORKSPACE or PKV_ERR_LAUNCH. */
 size_t beam_select_workspace_bytes(int B, int width, int V, int logits_fp32);
 int beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens, float* out_end,

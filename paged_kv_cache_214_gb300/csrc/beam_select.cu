@@ -646,7 +646,8 @@ SelectPlan plan_select(int B, int W, int V, bool f32, int sm_count) {
 int check_select(int B, int W, int V, int K) {
   if (B < 0 || W < 1 || V < 1 || K < 1) return PKV_ERR_ARG;
   if (W > kMaxWidth || K > kMaxOut) return PKV_ERR_SHAPE;
-  if (static_cast<int64_t>(W) * V > INT32_MAX - kSegment) return PKV_ERR_SHAPE;
+  // (a place in the row's last segment, or one segment on, is a 32-bit number too)
+  if (static_cast<int64_t>(W) * V > INT32_MAX - 2 * kSegment) return PKV_ERR_SHAPE;
   if (static_cast<int64_t>(B) * W > 65535) return PKV_ERR_SHAPE;
   return PKV_OK;
 }
