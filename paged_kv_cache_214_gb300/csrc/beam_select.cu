@@ -17,10 +17,14 @@
 // Work a logit: widening, maximum (three at a time), two multiply-adds (two at a time), one
 // 2^x, one addition (two at a time).
 //
-// Sums.  Scores of different beams are compared, so a row's sum has to be right to
-// far better than a score's own rounding.  2^(x log2(e) - C) with C = fl(m log2(e)) and
-// log2(e) as a sum of two fp32 numbers leaves only the roundings of single terms, about
-// 1e-8 of the sum; C itself cancels exactly, as the merge adds it back in 64 bits.
+// Sums.  Scores of different beams are compared, so a row's sum has to be right to better
+// than a score's own rounding.  2^(x log2(e) - C) with C = fl(m log2(e)) and log2(e) as a sum
+// of two fp32 numbers leaves the roundings of single terms (2^-22 and less) and of the additions
+// in fp32 (16 terms in two chains, a segment a step, five steps over the lanes); C itself cancels
+// exactly, as the merge adds it back in 64 bits, in which the warps' sums are joined too.
+// Measured against 64 bits, rows of 1000 to 150001 logits, flat, ordinary and with one token
+// that has half of the mass, around 0 and around 8000: off by 1e-7 (root of the mean square up
+// to 1.9e-7), 3.2e-7 at most.
 
 #include <cuda_bf16.h>
 #include <math.h>
