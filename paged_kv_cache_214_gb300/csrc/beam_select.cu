@@ -394,7 +394,7 @@ __device__ __forceinline__ void merge_request(const SelectParams& p, int b, Merg
     const float2 first = lane < parts ? __ldcg(st + lane) : make_float2(-INFINITY, 0.f);
     const float cum = p.scores[row];
     float at_eos = 0.f;
-    if (p.eos >= 0 && lane == 0)
+    if (p.eos >= 0 && lane == 0 && isfinite(cum))
       at_eos = kF32 ? static_cast<const float*>(p.logits)[row * p.row_stride + p.eos]
                     : __bfloat162float(static_cast<const __nv_bfloat16*>(
                           p.logits)[row * p.row_stride + p.eos]);
@@ -478,6 +478,14 @@ __device__ __forceinline__ void merge_request(const SelectParams& p, int b, Merg
   // not masked, 8 best: 330 us, 150 where all logits are equal; a pass over all beams for each
   // continuation took 2600 and 700.)
   auto next = [&](int w, float last_x, int last_v) {   // behind (last_x, last_v), into sm
+    if (!alive(w)) {   // (its logits are not read)
+      if (tid == 0) {
+        sm.next_i[w] = -1;
+        sm.next_s[w] = kNone;
+      }
+      __syncthreads();
+      return;
+    }
     const Row<kF32> in(p.logits, (static_cast<int64_t>(b) * W + w) * p.row_stride, p.V);
     constexpr int kWords = Row<kF32>::kWords;
     float x = -INFINITY;

@@ -58,3 +58,22 @@ def test_the_widest_vocabulary():
     assert (scores[0].cpu().double() - want).abs().max() <= 2.0 ** -11
     assert (end[0, 0].double() - (x[0, 0, V - 2].double() - total.log())).abs() <= 2.0 ** -11
     assert pkv.get_device_error() == pkv.PKV_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_beams_that_have_not_begun_beside_masses_of_equal_logits(dtype):
+    """Their logits are not read; whatever they hold, the live beam's come in their order."""
+    x = torch.full((2, 5, 5003), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+    x[..., 7] = 1.0
+    scores = torch.full((2, 5), -math.inf, device="cuda")
+    scores[0, 3], scores[1, 0], scores[1, 4] = -1.0, -2.0, -2.5
+    x[0, :3], x[0, 4], x[1, 1], x[1, 2], x[1, 3] = math.nan, 50.0, math.inf, -math.inf, 9.0
+    best, parents, tokens, end = pkv.beam_select(x, scores, 40, eos_token=2)
+    rest = [v for v in range(41) if v not in (2, 7)]
+    assert parents[0].tolist() == [3] * 40 and tokens[0].tolist() == [7] + rest[:39]
+    assert parents[1].tolist() == [0, 4] + [0] * 38 and tokens[1].tolist() == [7, 7] + rest[:38]
+    assert best[0, 0] == -1.0 and best[1, 0] == -2.0 and best[1, 1] == -2.5
+    live = torch.isfinite(scores)
+    assert (end[~live] == -math.inf).all() and (end[live] < -1e30).all()
+    assert pkv.get_device_error() == pkv.PKV_OK
