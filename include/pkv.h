@@ -651,8 +651,8 @@ int beam_select(float* out_scores, int32_t* out_parents, int32_t* out_tokens, fl
  * they must not overlap the inputs.  free_blocks: entries behind num_free are written.
  * A parent outside [-1, width) (taken as -1), a length outside the table (taken as 0), a
  * block id outside the pool (skipped) and a stack that runs empty or over are reported as
- * PKV_ERR_DEVICE_INDEX through pkv_get_device_error(); a row that gets no block of its own
- * becomes empty.
+ * PKV_ERR_DEVICE_INDEX through pkv_get_device_error(); a row that gets no block of its own, or
+ * whose copy has no source (it takes none then), becomes empty.
  * 1 <= width <= 32 (else PKV_ERR_SHAPE).  Returns as paged_append_tokens. */
 size_t paged_reorder_beams_workspace_bytes(int B, int width, int max_blocks_per_seq);
 int paged_reorder_beams(int32_t* out_tables, int32_t* out_lens, int32_t* copies,

@@ -288,7 +288,7 @@ constexpr int kColumns = 64;
 __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderParams p) {
   extern __shared__ int smem[];              // [W][kColumns] entries of the chunk, -1: none
   __shared__ int par[kMaxWidth], len[kMaxWidth], buf[64], flag;
-  __shared__ unsigned freed_rows[kColumns];
+  __shared__ unsigned freed_rows[kColumns], sourceless;   // (rows whose copy has no source)
   const int W = p.W, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x, R = p.B * W;
   const int row0 = b * W;
@@ -306,6 +306,7 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderP
     par[tid] = q;
     len[tid] = n;
   }
+  if (tid == 0) sourceless = 0;
   __syncthreads();
   // every thread: rows that have a child, and rows that are not their parent's first
   unsigned has_child = 0, later = 0;
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderP
       if ((later >> w & 1u) && len[from] / kBlockSize == column && len[from] % kBlockSize) {
         p.copies[row0 + w] = next;
         p.copies[2 * R + row0 + w] = next < 0 ? 0 : len[from] % kBlockSize;
+        if (next < 0) atomicOr(&sourceless, 1u << w);
         next = -1;
       }
       p.out_tables[static_cast<int64_t>(row0 + w) * p.maxblk + column] = next;
@@ -370,8 +372,15 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderP
   for (int w = 0; w < W; ++w)
     for (int c = done + tid; c < p.maxblk; c += kReorderThreads)
       p.out_tables[static_cast<int64_t>(row0 + w) * p.maxblk + c] = -1;
+  // a row that would copy a block which is none becomes empty (the chunks' entries are written),
+  // and takes no block off the stack
+  const unsigned gone_rows = sourceless;
+  for (unsigned left = gone_rows; left; left &= left - 1)
+    for (int c = tid; c < done; c += kReorderThreads)
+      p.out_tables[static_cast<int64_t>(row0 + __ffs(left) - 1) * p.maxblk + c] = -1;
   if (tid < W) {
-    const int row = row0 + tid, n = par[tid] < 0 ? 0 : len[par[tid]];
+    const bool gone = gone_rows >> tid & 1u;
+    const int row = row0 + tid, n = par[tid] < 0 || gone ? 0 : len[par[tid]];
     p.out_lens[row] = n;
     if (!(later >> tid & 1u) || n % kBlockSize == 0) {
       p.copies[row] = -1;
@@ -429,9 +438,8 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderP
       const long long i = top - 1 - e;
       int32_t* entries = p.out_tables + static_cast<int64_t>(row) * p.maxblk;
       const int column = __ldcg(p.out_lens + row) / kBlockSize;
-      const bool source = __ldcg(p.copies + row) >= 0;
       const int id = i >= 0 ? __ldcg(p.free_blocks + i) : -1;
-      if (id >= 0 && id < p.num_blocks && source) {
+      if (id >= 0 && id < p.num_blocks) {
         entries[column] = id;
         p.copies[R + row] = id;
       } else {   // none left: the row cannot go on
