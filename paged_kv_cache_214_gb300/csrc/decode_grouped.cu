@@ -367,7 +367,7 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
 // share of the tiles.
 struct Stream {
   float o[16][4];   // o[n][0..1] row gq, o[n][2..3] row gq + 8; columns: see out_dim
-  float m[2], l[2];
+  float m[2], l[2];   // reference of the weights (near the maximum), sum
 };
 
 // Dim of output column 2c + e of n-tile n.  E4M3 codes come in pairs, so a pair of
@@ -381,7 +381,11 @@ __device__ __forceinline__ int out_dim(int n, int c, int e) {
 // that rows gq and gq + 8 see; valid: tokens that any row sees (those behind hold
 // anything).  kSplit: weights with their rounded remainder.  kAll: the rows see all of them.
 //
-// Weights for the second product.  f16 (E4M3 pools): rounded once, off by 2^-11 at most.
+// Weights for the second product.  f16 (E4M3 pools): rounded once, off by 2^-11 at most.  f16
+// ends at 2^-25 (half its smallest step), so the largest weight is kept between 2^11 and 2^15:
+// a weight below 2^-25 of it has fewer bits and one below 2^-36 is lost (all of them together
+// 2^-14 of the sum in the longest table; with a largest weight of 1 four million keys of 2^-25.4
+// lost 8% of it).
 // bf16: up to 16 rows (MT = 1) carry the value and its rounded remainder, 16 significant
 // bits, as the decode does; more rows the value alone (off by 2^-8 at most, as in the
 // prefill), because a second set of products would hold up the copies.
@@ -390,6 +394,8 @@ __device__ __forceinline__ void consume_tokens(uint32_t kb, uint32_t vb, int t0,
                                                const uint32_t (&qa)[8][4], const float (&qmul)[2],
                                                const int (&lim)[2], int valid, Stream& st) {
   constexpr int NT = 2 * J;   // groups of 8 tokens
+  // log2 of the weight that a new maximum gets, and of the largest
+  constexpr float kTopWeight = kFp8 ? 11.f : 0.f, kMostWeight = kFp8 ? 15.f : 8.f;
   const int c = lane & 3;
   const int mi = lane >> 3, mr = lane & 7;   // ldmatrix: this lane gives row mr of matrix mi
   float sc[NT][4];
@@ -435,16 +441,16 @@ __device__ __forceinline__ void consume_tokens(uint32_t kb, uint32_t vb, int t0,
       }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // as in the decode, the maximum moves only when it rises by 2^8
-    if (top > st.m[r] + 8.f) {
-      const float alpha = rescale(st.m[r], top);
+    // as in the decode, the reference moves only when the maximum rises far above it
+    if (top > st.m[r] + kMostWeight) {
+      const float m = top - kTopWeight, alpha = rescale(st.m[r], m);
       st.l[r] *= alpha;
 #pragma unroll
       for (int n = 0; n < 16; ++n) {
         st.o[n][2 * r] *= alpha;
         st.o[n][2 * r + 1] *= alpha;
       }
-      st.m[r] = top;
+      st.m[r] = m;
     }
     const float ref = st.m[r] == -INFINITY ? 0.f : st.m[r];
 #pragma unroll
