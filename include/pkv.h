@@ -674,10 +674,10 @@ int kv_cache_copy_rows(void* k_cache, void* v_cache, const int32_t* copies, int 
 
 /* paged_decode_attention_grouped — paged_decode_attention in which each `width` consecutive
  * sequences are one request's: a block that several of them hold in the same column is
- * read once for all of them.  Results are those of paged_decode_attention on the same
- * arguments, whatever the tables share; lengths may differ and be 0.  The softmax weights
- * are rounded to 16 significant bits (bf16 pools, up to 16 query rows of a kv head and
- * request: width * Hq / Hkv), to 8 (bf16, more rows) or 11 (E4M3).  V of every position
+ * read once for all of them.  Results are paged_decode_attention's on the same arguments but
+ * for the order of sums, whatever the tables share; lengths may differ and be 0.  The softmax
+ * weights are rounded to 16 significant bits over bf16 pools, as there, and to 11 over E4M3
+ * pools (22 there), where those below 2^-36 of a row's largest may be dropped.  V of every position
  * that some sequence of a request sees must be finite (a hidden one enters the others'
  * sums with weight 0).
  * B rows in all, a multiple of width; 1 <= width <= 32, max_blocks_per_seq <= 16384 and

@@ -379,17 +379,20 @@ __device__ __forceinline__ int out_dim(int n, int c, int e) {
 
 // 16 J tokens of a tile from t0 on: kb, vb the tile's K and V.  lim: tokens of the tile
 // that rows gq and gq + 8 see; valid: tokens that any row sees (those behind hold
-// anything).  kSplit: weights with their rounded remainder.  kAll: the rows see all of them.
+// anything).  kAll: the rows see all of them.
 //
-// Weights for the second product.  f16 (E4M3 pools): rounded once, off by 2^-11 at most.  f16
+// Weights for the second product.  bf16 pools: the value and its rounded remainder, 16
+// significant bits, as the decode does, for any number of rows.  (The value alone, off by 2^-8 at
+// most, would take 85 us in place of 84 for 4 x 8 of 16k to 40k tokens, 32 rows, but 81 in place
+// of 101 for 4 x 12 of 8k to 20k, 48 rows, and for 1 x 16 of 30000, 128: the second set of
+// products holds up the copies there.)  E4M3 pools: f16, rounded once, off by 2^-11 at most; the
+// codes themselves are off by up to 2^-4 of what was stored, and the remainder (22 bits) would take
+// 74 us in place of 58 for 24 x 5 and 120 in place of 91 for 4 x 12.  f16
 // ends at 2^-25 (half its smallest step), so the largest weight is kept between 2^11 and 2^15:
 // a weight below 2^-25 of it has fewer bits and one below 2^-36 is lost (all of them together
 // 2^-14 of the sum in the longest table; with a largest weight of 1 four million keys of 2^-25.4
 // lost 8% of it).
-// bf16: up to 16 rows (MT = 1) carry the value and its rounded remainder, 16 significant
-// bits, as the decode does; more rows the value alone (off by 2^-8 at most, as in the
-// prefill), because a second set of products would hold up the copies.
-template <int J, bool kFp8, bool kSplit, bool kAll>
+template <int J, bool kFp8, bool kAll>
 __device__ __forceinline__ void consume_tokens(uint32_t kb, uint32_t vb, int t0, int lane,
                                                const uint32_t (&qa)[8][4], const float (&qmul)[2],
                                                const int (&lim)[2], int valid, Stream& st) {
@@ -466,16 +469,16 @@ __device__ __forceinline__ void consume_tokens(uint32_t kb, uint32_t vb, int t0,
   for (int j = 0; j < J; ++j) {   // 16 tokens a time
     uint32_t ph[4], pl[4];
     const float (&x)[4] = sc[2 * j], (&y)[4] = sc[2 * j + 1];
-    if constexpr (kSplit) {
+    if constexpr (kFp8) {
+      ph[0] = pack_f16x2(x[0], x[1]);
+      ph[1] = pack_f16x2(x[2], x[3]);
+      ph[2] = pack_f16x2(y[0], y[1]);
+      ph[3] = pack_f16x2(y[2], y[3]);
+    } else {
       split_pair<false>(x[0], x[1], ph[0], pl[0]);
       split_pair<false>(x[2], x[3], ph[1], pl[1]);
       split_pair<false>(y[0], y[1], ph[2], pl[2]);
       split_pair<false>(y[2], y[3], ph[3], pl[3]);
-    } else {
-      ph[0] = kFp8 ? pack_f16x2(x[0], x[1]) : pack_bf16x2(x[0], x[1]);
-      ph[1] = kFp8 ? pack_f16x2(x[2], x[3]) : pack_bf16x2(x[2], x[3]);
-      ph[2] = kFp8 ? pack_f16x2(y[0], y[1]) : pack_bf16x2(y[0], y[1]);
-      ph[3] = kFp8 ? pack_f16x2(y[2], y[3]) : pack_bf16x2(y[2], y[3]);
     }
     // tokens behind the last one that any row sees are zeroed: they may hold NaN patterns
     const int tj = t0 + 16 * j;
@@ -513,8 +516,7 @@ __device__ __forceinline__ void consume_tokens(uint32_t kb, uint32_t vb, int t0,
         } else {
           const int n = 2 * i + h;
           mma_16x8x16<false>(st.o[n], ph[0], ph[1], ph[2], ph[3], r[2 * h], r[2 * h + 1]);
-          if constexpr (kSplit)
-            mma_16x8x16<false>(st.o[n], pl[0], pl[1], pl[2], pl[3], r[2 * h], r[2 * h + 1]);
+          mma_16x8x16<false>(st.o[n], pl[0], pl[1], pl[2], pl[3], r[2 * h], r[2 * h + 1]);
         }
       }
     }
@@ -788,22 +790,21 @@ __device__ __forceinline__ void serve(const CUtensorMap* kmap, const CUtensorMap
         // (rows that are not there: no limit, so that they do not count; nobody reads them)
         const int lim[2] = {tile.y & bit[0] ? len[0] - pos : 0, tile.y & bit[1] ? len[1] - pos : 0};
         const uint32_t kb = smem_addr(smem + s * L::kStageBytes);
-        // up to 32 tokens at a time (64 would not leave the registers for the scores).  Most tiles
-        // are of a prompt, which every row sees whole: without the comparisons and the zeroing of
-        // what lies behind a length, 16 rows of 8 heads over 30000 tokens take 81 us, not 90, and
-        // 24 x 5 E4M3 rows 59.6, not 61.1; narrow groups the same
-        constexpr int J = MT < 2 ? MT : 2;
-        constexpr bool kSplit = MT == 1 && !kFp8;
+        // Up to 32 tokens at a time (64 would not leave the registers for the scores), 16 with 32
+        // bf16 rows (4 x 8 sequences of 16k to 40k tokens 84 us, 32 at a time 90; with 64 rows 4 x
+        // 12 of 8k to 20k 107 and 101).  Most tiles are of a prompt, which every row sees whole:
+        // without the comparisons and the zeroing of what lies behind a length, 16 rows of 8 heads
+        // over 30000 tokens take a tenth less, 24 x 5 E4M3 rows 59.6 us, not 61.1; narrow groups the
+        // same
+        constexpr int J = MT == 1 || (MT == 2 && !kFp8) ? 1 : 2;
         if (__all_sync(0xffffffffu, min(lim[0], lim[1]) >= kTile)) {
 #pragma unroll 1
           for (int t = t0; t < t0 + 16 * MT; t += 16 * J)
-            consume_tokens<J, kFp8, kSplit, true>(kb, kb + L::kOpBytes, t, lane, qa, qmul, lim, kTile,
-                                                  st);
+            consume_tokens<J, kFp8, true>(kb, kb + L::kOpBytes, t, lane, qa, qmul, lim, kTile, st);
         } else {
 #pragma unroll 1
           for (int t = t0; t < t0 + 16 * MT && t < valid; t += 16 * J)
-            consume_tokens<J, kFp8, kSplit, false>(kb, kb + L::kOpBytes, t, lane, qa, qmul, lim, valid,
-                                                   st);
+            consume_tokens<J, kFp8, false>(kb, kb + L::kOpBytes, t, lane, qa, qmul, lim, valid, st);
         }
       }
       __syncwarp();
