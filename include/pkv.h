@@ -677,9 +677,9 @@ int kv_cache_copy_rows(void* k_cache, void* v_cache, const int32_t* copies, int 
  * read once for all of them.  Results are paged_decode_attention's on the same arguments but
  * for the order of sums, whatever the tables share; lengths may differ and be 0.  The softmax
  * weights are rounded to 16 significant bits over bf16 pools, as there, and to 11 over E4M3
- * pools (22 there), where those below 2^-36 of a row's largest may be dropped.  V of every position
- * that some sequence of a request sees must be finite (a hidden one enters the others'
- * sums with weight 0).
+ * pools (22 there), where those below 2^-36 of a row's largest may be dropped.  A value that
+ * is not finite reaches the sequences that see its position and no others (where some of a
+ * request's do not see it the call takes 1 to 25 times as long, as they are attended to one by one).
  * B rows in all, a multiple of width; 1 <= width <= 32, max_blocks_per_seq <= 16384 and
  * B * max_blocks_per_seq <= 2^27 (else PKV_ERR_SHAPE).  num_splits: ranges that a request's
  * blocks are cut into (0: automatic).  workspace: paged_decode_grouped_workspace_bytes of

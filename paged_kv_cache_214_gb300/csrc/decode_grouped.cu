@@ -95,6 +95,9 @@ struct GroupedParams {
   __nv_bfloat16* out;
   float* lse;
   const __nv_bfloat16* q;
+  const void* k_cache;
+  const void* v_cache;
+  uint32_t num_blocks;
   const int32_t* context_lens;
   float* ws_o;         // [2 x thread blocks, rows, 128] normalised partial outputs
   float* ws_lse;       // [2 x thread blocks, rows] log2-sum-exps
@@ -347,8 +350,8 @@ struct GroupedLayout {
   static constexpr int kMergeM = kTiles + kStages * 16;   // [4][16]
   static constexpr int kMergeL = kMergeM + 64 * 4;
   static constexpr int kBars = kMergeL + 64 * 4;
-  static constexpr int kFlags = kBars + 2 * kStages * 8;   // abort, last, issued
-  static constexpr int kBytes = kFlags + 16 + 1024;             // + alignment slack
+  static constexpr int kFlags = kBars + 2 * kStages * 8;   // abort, last, issued, again; partly [4]
+  static constexpr int kBytes = kFlags + 32 + 1024;             // + alignment slack
   static_assert(kBytes <= 113 * 1024, "two blocks per SM");
 };
 
@@ -557,6 +560,93 @@ __device__ __forceinline__ float f16_q(uint32_t (&qa)[8][4], int r, float scale_
       x = pack_f16x2(bf16lo(x) * up, bf16hi(x) * up);
     }
   return scale_log2 * k_scale * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
+}
+
+// By one warp: a row alone over the tiles of a segment's list, from global memory (see serve()).
+// q: the row; w: its sequence in the group; len: its length; lane: dims 4 lane and on.  Leaves
+// the output against the reference m and the sum l.
+template <bool kFp8>
+__device__ __forceinline__ void attend_alone(const GroupedParams& p, int64_t list, int count, int kvh,
+                                             const __nv_bfloat16* q, int w, int len, float4& o,
+                                             float& m, float& l) {
+  const int lane = threadIdx.x & 31;
+  auto four = [&](const void* pool, int64_t slot) {
+    const int64_t at = (slot * p.Hkv + kvh) * kHeadDim + 4 * lane;
+    if constexpr (kFp8) {
+      const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(pool) + at);
+      float4 v;
+      f16x2_unpack(e4m3x2_lo_to_f16x2(x), v.x, v.y);
+      f16x2_unpack(e4m3x2_hi_to_f16x2(x), v.z, v.w);
+      return v;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(pool) + at);
+      return make_float4(bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y));
+    }
+  };
+  const uint2 qw = *reinterpret_cast<const uint2*>(q + 4 * lane);
+  const float mul = p.scale_log2 * (kFp8 ? p.k_scale : 1.f);
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < count; ++i) {
+    const uint32_t word = p.plan.word[list + i];
+    // (no block of this pool: not a plan of these arguments, see tiles_of())
+    if (!(p.plan.mask[list + i] >> w & 1u) || word >> 9 >= p.num_blocks) continue;
+    const int k = word >> 7 & 3;
+    const int n = min(kTile, len - (p.plan.column[list + i] * kBlockSize + k * kTile));
+    const int64_t slot = static_cast<int64_t>(word >> 9) * kBlockSize + k * kTile;
+#pragma unroll 1
+    for (int t0 = 0; t0 < n; t0 += 32) {
+      float s = -INFINITY;   // of token t0 + lane
+      const int tokens = min(32, n - t0);
+      float4 x[8];   // (on their way at a time; those behind the last one are the last again)
+      auto eight = [&](const void* pool, int t) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = four(pool, slot + t0 + min(t + j, tokens - 1));
+      };
+#pragma unroll 1
+      for (int t = 0; t < tokens; t += 8) {
+        eight(p.k_cache, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float d = bf16lo(qw.x) * x[j].x + bf16hi(qw.x) * x[j].y + bf16lo(qw.y) * x[j].z +
+                    bf16hi(qw.y) * x[j].w;
+#pragma unroll
+          for (int sh = 16; sh; sh >>= 1) d += __shfl_xor_sync(0xffffffffu, d, sh);
+          if (lane == t + j && lane < tokens) s = d * mul;
+        }
+      }
+      float top = s;
+#pragma unroll
+      for (int sh = 16; sh; sh >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sh));
+      if (top > m) {
+        const float alpha = rescale(m, top);
+        l *= alpha;
+        o.x *= alpha;
+        o.y *= alpha;
+        o.z *= alpha;
+        o.w *= alpha;
+        m = top;
+      }
+      const float e = lane < tokens ? ex2(s - (m == -INFINITY ? 0.f : m)) : 0.f;
+      l += e;
+#pragma unroll 1
+      for (int t = 0; t < tokens; t += 8) {
+        eight(p.v_cache, t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float weight = __shfl_sync(0xffffffffu, e, (t + j) & 31);
+          o.x = fmaf(weight, x[j].x, o.x);
+          o.y = fmaf(weight, x[j].y, o.y);
+          o.z = fmaf(weight, x[j].z, o.z);
+          o.w = fmaf(weight, x[j].w, o.w);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int sh = 16; sh; sh >>= 1) l += __shfl_xor_sync(0xffffffffu, l, sh);
 }
 
 // By one warp: the output of a row without keys.
@@ -774,6 +864,8 @@ __device__ __forceinline__ void serve(const CUtensorMap* kmap, const CUtensorMap
     for (int n = 0; n < 16; ++n) st.o[n][0] = st.o[n][1] = st.o[n][2] = st.o[n][3] = 0.f;
     st.m[0] = st.m[1] = -INFINITY;
     st.l[0] = st.l[1] = 0.f;
+    volatile int& partly = flags[4 + warp];   // some row did not see all of some tile
+    if (lane == 0) partly = 0;
     for (int i = 0; i < seg.count; ++i) {
       const int it = seg.before + i, s = it % L::kStages;
       if (flags[0]) break;
@@ -802,6 +894,7 @@ __device__ __forceinline__ void serve(const CUtensorMap* kmap, const CUtensorMap
           for (int t = t0; t < t0 + 16 * MT; t += 16 * J)
             consume_tokens<J, kFp8, true>(kb, kb + L::kOpBytes, t, lane, qa, qmul, lim, kTile, st);
         } else {
+          if (lane == 0) partly = 1;
 #pragma unroll 1
           for (int t = t0; t < t0 + 16 * MT && t < valid; t += 16 * J)
             consume_tokens<J, kFp8, false>(kb, kb + L::kOpBytes, t, lane, qa, qmul, lim, valid, st);
@@ -810,6 +903,19 @@ __device__ __forceinline__ void serve(const CUtensorMap* kmap, const CUtensorMap
       __syncwarp();
       if (lane == 0) mbar_arrive(empty_bar(s));
     }
+    // The weight 0 of a token that a row does not see, times a value that is not finite, is NaN.
+    // That is rare, and testing the values in the loop cost 4 x 8 of 16k to 40k tokens 13 us
+    // and 24 x 5 E4M3 21, so the outputs are tested here; with a NaN among them the segment's
+    // rows are worked out again, each by itself (one NaN in a beam's page: 16 x 4 0.5 ms, 4 x 8 of
+    // 16k to 40k 1.9 ms).
+    float z[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < 16; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[e >> 1] = fmaf(st.o[n][e], 0.f, z[e >> 1]);
+    __syncwarp();
+    if (partly && ((16 * mt + gq < n_rows && z[0] != 0.f) || (16 * mt + 8 + gq < n_rows && z[1] != 0.f)))
+      flags[3] = 1;
     __syncwarp();
   }
   __syncthreads();   // every warp is done with the ring, and every copy was waited for,
@@ -827,7 +933,23 @@ __device__ __forceinline__ void serve(const CUtensorMap* kmap, const CUtensorMap
   }
 
   // ---------------------------------------------------------------- epilogue
-  if (consumer) {
+  const bool again = flags[3] && !flags[0];
+  if (again) {   // (each row in the place of its first share, the others empty)
+    const int64_t list = static_cast<int64_t>(seg.unit) * p.plan.most + seg.begin;
+    for (int r = warp; r < n_rows; r += kWarpsN) {
+      const int w = r / n_heads, len = min(max(p.context_lens[first_row + w], 0), p.max_len);
+      float4 o;
+      float m, l;
+      attend_alone<kFp8>(p, list, seg.count, kvh, p.q + out_row(r) * kHeadDim, w, len, o, m, l);
+      for (int k = 0; k < 4 / MT; ++k) {
+        const int row = 16 * (k * MT + r / 16) + r % 16;
+        reinterpret_cast<float4*>(merge_o + row * kHeadDim)[lane] =
+            k ? make_float4(0.f, 0.f, 0.f, 0.f) : o;
+        merge_m[row] = k ? -INFINITY : m;
+        merge_l[row] = k ? 0.f : l;
+      }
+    }
+  } else if (consumer) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       st.l[r] += __shfl_xor_sync(0xffffffffu, st.l[r], 1);
@@ -851,6 +973,7 @@ __device__ __forceinline__ void serve(const CUtensorMap* kmap, const CUtensorMap
     }
   }
   __syncthreads();
+  if (tid == 0) flags[3] = 0;   // (before the next segment's first barrier)
   // a warp a row, a lane four dims
   const int stride_rows = p.units.seqs * p.heads;   // rows of a partial result
   const int64_t part0 =
@@ -990,7 +1113,7 @@ grouped_decode_kernel(const __grid_constant__ CUtensorMap kmap,
       mbar_init(bars + 8u * s, 1);
       mbar_init(bars + 8u * (L::kStages + s), L::kConsumers);
     }
-    flags[0] = flags[1] = flags[2] = 0;
+    flags[0] = flags[1] = flags[2] = flags[3] = 0;
     fence_barrier_init();
   }
   // May start while the plan is being made, and lets the next kernel start (see
@@ -1144,6 +1267,9 @@ int grouped_entry(const DecodeArgs& a, int width, int D, int block_size, int pla
   prm.out = static_cast<__nv_bfloat16*>(a.out);
   prm.lse = a.lse;
   prm.q = static_cast<const __nv_bfloat16*>(a.q);
+  prm.k_cache = a.k_cache;
+  prm.v_cache = a.v_cache;
+  prm.num_blocks = static_cast<uint32_t>(a.num_blocks);
   prm.context_lens = a.context_lens;
   prm.ws_count = reinterpret_cast<unsigned*>(ws);
   const int64_t y = static_cast<int64_t>(a.Hkv) * plan.head_groups;
