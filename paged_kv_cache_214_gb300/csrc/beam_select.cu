@@ -48,8 +48,6 @@ constexpr double kLn2d = 0.69314718055994530942;
 // so 2^(x log2(e) - C) stays near 1 for x = m.
 constexpr float kFar = 8192.f;
 
-inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-
 struct SelectParams {
   float* out_scores;
   int32_t* out_parents;
@@ -649,9 +647,9 @@ SelectPlan plan_select(int B, int W, int V, bool f32, int sm_count) {
   plan.share = (segments + n - 1) / n;
   plan.blocks = (segments + plan.share - 1) / plan.share;
   plan.pieces = (plan.segments - 1) / plan.share + 2;
-  plan.stats_bytes = align256(static_cast<size_t>(rows) * plan.pieces * kWarps * 8);
+  plan.stats_bytes = align_up(static_cast<size_t>(rows) * plan.pieces * kWarps * 8, 256);
   plan.workspace_bytes = kWorkspaceCounterBytes + plan.stats_bytes +
-                         align256(static_cast<size_t>(rows) * plan.segments * 4);
+                         align_up(static_cast<size_t>(rows) * plan.segments * 4, 256);
   return plan;
 }
 

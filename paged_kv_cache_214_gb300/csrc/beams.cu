@@ -20,8 +20,6 @@ namespace {
 
 constexpr int kMaxRows = 8192;   // rows whose prefix sums a thread block keeps
 
-inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
-
 // Exclusive prefix sums of two values over the block's threads, and their totals.
 // `buf`: 2 * 32 values.
 template <typename T>
@@ -457,8 +455,8 @@ __global__ void __launch_bounds__(kReorderThreads) reorder_kernel(const ReorderP
 }
 
 size_t reorder_workspace(int B, int W, int maxblk) {
-  return kWorkspaceCounterBytes + 2 * align256(static_cast<size_t>(B) * 4) +
-         align256(static_cast<size_t>(B) * W * maxblk * 4);
+  return kWorkspaceCounterBytes + 2 * align_up(static_cast<size_t>(B) * 4, 256) +
+         align_up(static_cast<size_t>(B) * W * maxblk * 4, 256);
 }
 
 // ------------------------------------------------------------------ row copies
@@ -618,7 +616,7 @@ extern "C" int paged_reorder_beams(int32_t* out_tables, int32_t* out_lens, int32
   unsigned* err = device_error_word();
   if (!err) return PKV_ERR_LAUNCH;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t list = align256(static_cast<size_t>(B) * 4);
+  const size_t list = align_up(static_cast<size_t>(B) * 4, 256);
   const ReorderParams p{out_tables, out_lens, copies, out_num_free, block_tables, context_lens,
                         parents, kept_blocks, free_blocks, num_free, B, width,
                         max_blocks_per_seq, static_cast<int>(num_blocks),

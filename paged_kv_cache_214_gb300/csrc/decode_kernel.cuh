@@ -998,8 +998,6 @@ inline bool decode_maps(const DecodeArgs& a, CUtensorMap* km, CUtensorMap* vm) {
          encode_pool_map(vm, a.v_cache, slots, a.Hkv, kTile);
 }
 
-inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 // Kernel parameters of a call, apart from the score options.
 inline DecodeParams decode_params(const DecodeArgs& a, const DecodePlan& plan, unsigned* err) {
   DecodeParams prm = {};

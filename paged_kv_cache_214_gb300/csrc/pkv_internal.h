@@ -23,6 +23,7 @@ constexpr int kMaxWidth = 32;
 
 // SM count of the current device (cached per device); 0 on failure.
 int device_sm_count();
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // Whether a call's workspace holds `need` bytes and is aligned.
 inline bool workspace_fits(const void* ws, size_t have, size_t need) {
   return need == 0 || (ws && have >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
