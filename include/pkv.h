@@ -680,6 +680,11 @@ int kv_cache_copy_rows(void* k_cache, void* v_cache, const int32_t* copies, int 
  * pools (22 there), where those below 2^-36 of a row's largest may be dropped.  A value that
  * is not finite reaches the sequences that see its position and no others (where some of a
  * request's do not see it the call takes 1 to 25 times as long, as they are attended to one by one).
+ * When it pays: where reading shared blocks once saves much, from about 100 MB a call over bf16
+ * pools (16 requests x 2 sequences of 2000 tokens, 8 kv heads: 38 us against 45) and 50 MB over
+ * E4M3 pools (the same: 31 against 38).  With one sequence a request, a single request of a few
+ * thousand tokens, or many short sequences (4 x 16 of 500) paged_decode_attention takes as long
+ * or half as long.
  * B rows in all, a multiple of width; 1 <= width <= 32, max_blocks_per_seq <= 16384 and
  * B * max_blocks_per_seq <= 2^27 (else PKV_ERR_SHAPE).  num_splits: ranges that a request's
  * blocks are cut into (0: automatic).  workspace: paged_decode_grouped_workspace_bytes of

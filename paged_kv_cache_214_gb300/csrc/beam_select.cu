@@ -10,10 +10,10 @@
 // reads the segments that reach it again (K or a few more, K KB and mostly from L2) and
 // ranks the logits that do.  Bounds are compared in fp32 with a margin for its rounding,
 // candidates ranked by their score in 64 bits.
-// 64 x 8 rows of 150001 bf16 logits, 154 MB, 16 best: 40 us a call of a graph (floor 23), 29 of
+// 64 x 8 rows of 150001 bf16 logits, 154 MB, 16 best: 41 us a call of a graph (floor 23), 29 of
 // them the pass (5.3 TB/s; issue 55%, 2^x 25%), the rest the last block's work, in which
-// the other SMs idle.  4 rows of 32000: 10.6 us, a chain of dependent steps.  Two, four or
-// five thread blocks an SM took 51, 43 and 43 us in place of 40.
+// the other SMs idle.  4 rows of 32000: 10.2 us, a chain of dependent steps.  Two, four or
+// five thread blocks an SM took 51, 43 and 43 us where three took 40.
 // Work a logit: widening, maximum (three at a time), two multiply-adds (two at a time), one
 // 2^x, one addition (two at a time).
 //

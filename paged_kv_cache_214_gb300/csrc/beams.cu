@@ -7,10 +7,10 @@
 // thread block works out the prefix sums that it needs for itself, and what depends on all
 // blocks (lengths written in place, the stack of free blocks) is left to the last one
 // to arrive: one launch, nothing spins, and the order of the stack follows from the
-// inputs alone.  A call of a graph of many: appending a token to 256 sequences 3.6 us, up to
-// 1500 tokens to 48 sequences 5.1; reordering 1 x 4 / 64 x 4 / 20 x 12 rows 5.2, 7.8 and 9.6
+// inputs alone.  A call of a graph of many: appending a token to 256 sequences 3.9 us, up to
+// 1500 tokens to 48 sequences 5.8; reordering 1 x 4 / 64 x 4 / 20 x 12 rows 5.5, 7.8 and 9.5
 // us (tables, lengths and stack are under 1 MB).  The copies are bound by memory where there
-// are many: 55 MB read and 55 written in 12.1 us (the writes stay in L2).
+// are many: 55 MB read and 55 written in 11.5 us (the writes stay in L2).
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"

@@ -27,21 +27,24 @@
 //   output and the queries of 16 rows in registers and K and V leave shared memory MT
 //   times.  Both products run on the warp-level MMA (m16n8k16, fp32 accumulation),
 //   operands by ldmatrix; E4M3 codes are converted to f16, exactly.  With at most 64 rows
-//   a byte of K/V carries at most 128 operations, a sixth of the warp-level MMA's rate at the
-//   copy bandwidth.  Up to 32 bf16 rows HBM is the bound while tiles stream, beyond, and over
-//   E4M3 codes, the softmax and the conversions between the products are, as below.
+//   a byte of bf16 K carries at most 64 operations and one of V 128 (weights in two parts), a
+//   sixth of the warp-level MMA's rate at the copy bandwidth.  Up to 32 bf16 rows HBM is the
+//   bound while tiles stream, beyond, and over E4M3 codes, the products, the softmax and the
+//   conversions between them are, as below.
 //   Rows that do not hold a tile, and positions behind a row's length, score -inf.
 //   The shares are merged through shared memory, the ranges through the workspace by the
 //   last block to arrive, as in the decode, many of them in two steps.
 //
 // Measured (one call of a graph of many, inputs in memory; floor: the distinct blocks' bytes
-// at the copy bandwidth).  4 x 8 sequences of 16k to 40k tokens, 32 / 8 heads, 415 MB: 85
+// at the copy bandwidth).  4 x 8 sequences of 16k to 40k tokens, 32 / 8 heads, 415 MB: 84
 // us (floor 62), 4.9 TB/s; 16 x 4 of 512 to 4700, 238 MB: 52 us (36), 7.7 TB/s inside the
 // loop over tiles, with 20 us around it: the plan (5), lengths and the first copy (5), both
-// merges (8).  24 x 5 E4M3, 35 rows a kv head, 78 MB: 58 us (12): 2.0 us a tile of 64 tokens
-// that all rows see and 1.5 us one of a single sequence, of code conversion, products
-// and softmax in a chain of dependent instructions (issue 28%, tensor pipe 24%), three
-// warps of four with rows.
+// merges (8).  4 x 12 of 8k to 20k, 48 rows in a tile of 64: 104 us (47), 1 x 16 of 30000, 64 / 8
+// heads, 128 rows: 102 (22).  24 x 5 E4M3, 35 rows a kv head, 78 MB: 58 us (12): 2.0 us a tile
+// of 64 tokens that all rows see and 1.5 us one of a single sequence, of code conversion,
+// products and softmax in a chain of dependent instructions (issue 28%, tensor pipe 24%), three
+// warps of four with rows.  One sequence after the other (paged_decode_attention) the same calls
+// take 276, 85, 254, 213 and 243 us.
 
 #include <cmath>
 
