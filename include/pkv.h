@@ -614,7 +614,8 @@ int paged_append_tokens(int32_t* slot_mapping, int32_t* positions, int32_t* cu_s
  * beam's logarithm is kept to a few 1e-7 (fp32 terms and additions; measured up to 3.2e-7,
  * 1e-7 on average, for rows of 1000 to 150001 logits), so that scores of different beams that
  * lie closer than about 6e-7 may come in either order, also those of two beams with the
- * same logits; a beam's own continuations always come in the order of their logits.  Places for which there is no continuation get score -inf, parent
+ * same logits; those of one beam come in the order of their logits (compared by their scores
+ * in 64 bits).  Places for which there is no continuation get score -inf, parent
  * -1 and token -1.
  *   eos_token >= 0: that token ends a sequence.  It is not among the continuations (its
  *     probability counts in the sum), and out_end[b, w] (fp32 [B, width]) is the score of
